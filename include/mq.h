@@ -215,6 +215,125 @@ int mq_mlp_w4a4(const void *x, int64_t M, int64_t K,
                 void *y, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * y = x W^T with x left in bf16 and W the NVFP4 weight that mq_linear_w4a4
+ * takes: the linear of a decode step that does not quantize its activation
+ * ("精确解码", precise decoding: only the prefill runs W4A4; section 方法步骤详情
+ * of the paper.rainbus.top digest, section Method of the r9-hu digest).
+ *   y[m, n] = bf16( alpha_w * sum_k x[m, k] (sigma q)_w[n, k] )
+ * with exact products and binary32 sums.
+ *   x        : device bf16 [M, K], 1 <= M <= MQ_LINEAR_W4A16_MAX_M (more
+ *              rows: MQ_ERR_SHAPE; they are mq_linear_w4a4's)
+ *   w_codes, w_scales, alpha_w : quantized W [N, K]
+ *   y        : device bf16 [M, N], written
+ */
+#define MQ_LINEAR_W4A16_MAX_M 64
+int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
+                    const uint8_t *w_codes, const uint8_t *w_scales, const float *alpha_w, int64_t N,
+                    void *y, void *stream);
+
+/*
+ * What stands between the QKV and the O linear: rotary positions, the KV
+ * cache that the prefill writes and the decode phase reads (the pages' "KV
+ * cache" of the initial context, section 方法步骤详情, step (4); they give it no
+ * numerics, so the 8-bit form is this library's), and the attention over it.
+ *
+ * mq_kv_cache: a pool of pages of page_size tokens, for K and for V
+ *   codes  : [num_pages][kv_heads][page_size][head_dim] E4M3 bytes (16-byte aligned)
+ *   scales : [num_pages][kv_heads] floats, each a power of two 2^e,
+ *            -96 <= e <= 119; the value of a code c is 2^e c
+ *   page_size 16, 32, 64 or 128; head_dim 64 or 128
+ *
+ * mq_kv_batch: the sequences of one call, all device arrays of int32
+ *   cu_rows    : [batch + 1], the new tokens of sequence b are the rows
+ *                cu_rows[b] .. cu_rows[b + 1] - 1 of the row tensors; rows
+ *                from cu_rows[batch] on belong to nobody: never written
+ *   lens       : [batch], the sequence's length with its new tokens; its row
+ *                i has position lens[b] - (cu_rows[b + 1] - cu_rows[b]) + i
+ *                (rows with a negative position are padding in front: append
+ *                leaves them, attention sees no key for them)
+ *   page_table : [batch][max_pages], the page of positions
+ *                [i page_size, (i + 1) page_size); entries that no position
+ *                below lens[b] needs are not looked at
+ *   Several sequences may name the same page, but a page that a call appends
+ *   to belongs to one sequence.
+ *
+ * mq_rope_kv_append: for every new token, from its row of the QKV product
+ * [q heads | k heads | v heads] x head_dim
+ *   q_out = bf16(rot(q)), and rot(k), v appended to the cache.
+ *   rot    : the first rot_dim elements of a head in pairs (a, b) =
+ *            (x_j, x_{j + rot_dim/2}), or (x_{2j}, x_{2j+1}) if interleaved:
+ *              a' = fl32(fl32(a cos) - fl32(b sin)), b' = fl32(fl32(b cos) + fl32(a sin))
+ *            cos, sin from rope[position][j] and rope[position][rot_dim/2 + j];
+ *            rot_dim a multiple of 16, 0 .. head_dim (0: rope may be NULL)
+ *   codes  : RNE_E4M3_satfinite(x / 2^e), e the least with max |x| <= 448 * 2^e
+ *            (clamped to the range above) over the call's tokens in the
+ *            page, of that head.  A page that holds earlier tokens of the
+ *            sequence keeps the larger of its scale and this one; where it
+ *            grows, the earlier codes are rescaled and rounded again (exact
+ *            but for codes that turn subnormal).
+ *   qkv    : device bf16 [T, row_stride], row_stride >= (q_heads + 2 kv_heads)
+ *            head_dim, a multiple of 8
+ *   rope   : device float [max_pos][rot_dim], 16-byte aligned
+ *   q_out  : device bf16 [T, q_heads, head_dim], written
+ *   ws     : optional workspace (256-byte header) whose status word takes
+ *            MQ_ERR_INVALID_ARG when a position, a page number or a length is
+ *            outside the tables: what it concerns is not written
+ *   NaN in k or v: the rows that see the token become NaN, no others.
+ *   Infinities saturate.
+ *
+ * mq_kv_attention: for the new token of row r at position p of its sequence, head h
+ *   out[r, h] = sum_j softmax_j(scale q[r, h] . k[j]) v[j], j = 0 .. min(p, lens[b] - 1),
+ * k, v of kv head h / (q_heads / kv_heads); zero where there is no j.
+ * Products are of f16 operands (the cache's codes are exact in f16, q goes to
+ * f16 under a power of two per row, the softmax weights round to f16), sums
+ * and statistics in binary32, the output rounded once to bf16.
+ *   q       : device bf16 [T, q_row_stride], a row's heads at its front;
+ *             q_row_stride >= q_heads head_dim, a multiple of 8
+ *   out     : device bf16 [T, q_heads, head_dim], written
+ *   q_heads : a multiple of kv_heads, at most 128 times as many
+ *   max_q, max_len : no sequence has more new tokens, or a greater length
+ *             (host values, e.g. fixed for a captured graph; one that has
+ *             more sets MQ_ERR_INVALID_ARG in the workspace's status word and
+ *             its rows are not written)
+ *   scale   : finite and positive
+ *   ws      : >= mq_kv_attention_workspace_bytes(batch, q_heads, kv_heads,
+ *             head_dim, max_q, max_len) bytes, 256-byte aligned, zero-filled
+ *             before its first use and used by mq_kv_attention alone (calls
+ *             of any sizes may follow one another on it); calls sharing it
+ *             must not overlap on the GPU
+ */
+typedef struct mq_kv_cache {
+    uint8_t *k_codes;
+    uint8_t *v_codes;
+    float *k_scales;
+    float *v_scales;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t reserved;      /* 0 */
+} mq_kv_cache;
+
+typedef struct mq_kv_batch {
+    const int32_t *cu_rows;
+    const int32_t *lens;
+    const int32_t *page_table;
+    int64_t max_pages;
+    int32_t batch;
+    int32_t reserved;      /* 0 */
+} mq_kv_batch;
+
+int mq_rope_kv_append(const void *qkv, int64_t T, int64_t row_stride, int32_t q_heads,
+                      const float *rope, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                      const mq_kv_cache *cache, const mq_kv_batch *batch,
+                      void *q_out, void *ws, size_t ws_bytes, void *stream);
+size_t mq_kv_attention_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int64_t max_q, int64_t max_len);
+int mq_kv_attention(const void *q, int64_t T, int64_t q_row_stride, int32_t q_heads,
+                    const mq_kv_cache *cache, const mq_kv_batch *batch, int64_t max_q, int64_t max_len,
+                    float scale, void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * mq_linear_w4a4 for callers that cannot allocate device memory -- for
  * example a plugin inside a host application that owns all device memory and
  * hands extensions no allocator, or C code that must not call cudaMalloc

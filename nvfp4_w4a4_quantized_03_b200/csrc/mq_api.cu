@@ -8,6 +8,7 @@
 
 #include "../../include/mq.h"
 #include "mq_internal.h"
+#include "mq_kv_plan.h"
 
 namespace {
 
@@ -370,6 +371,104 @@ int mq_mlp_w4a4(const void* x, int64_t M, int64_t K, const uint8_t* wgu_codes, c
     return cuda_status(e);
 }
 
+int mq_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8_t* w_codes, const uint8_t* w_scales,
+                    const float* alpha_w, int64_t N, void* y, void* stream) {
+    if (!x || !w_codes || !w_scales || !alpha_w || !y) return MQ_ERR_INVALID_ARG;
+    int st = check_rows_k(N, K);
+    if (st != MQ_OK) return st;
+    // rows of W and the tiles that cover them are counted in 32 bits
+    if (M < 1 || M > MQ_LINEAR_W4A16_MAX_M || N > 0x7fffff00) return MQ_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y) ||
+        (reinterpret_cast<uintptr_t>(alpha_w) & 3u))
+        return MQ_ERR_ALIGN;
+    int sms = 0;
+    st = current_device_info(&sms);
+    if (st != MQ_OK) return st;
+    return cuda_status(mq::launch_linear_w4a16(x, M, K, w_codes, w_scales, alpha_w, N, y, sms,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+// What mq_rope_kv_append and mq_kv_attention ask of a cache, a batch and the heads.
+static int check_kv(const mq_kv_cache* c, const mq_kv_batch* b, int64_t T, int32_t q_heads) {
+    if (!c || !b || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !b->cu_rows || !b->lens ||
+        !b->page_table)
+        return MQ_ERR_INVALID_ARG;
+    if (c->reserved != 0 || b->reserved != 0) return MQ_ERR_INVALID_ARG;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return MQ_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return MQ_ERR_SHAPE;
+    if (c->kv_heads < 1 || c->kv_heads > 1024 || c->num_pages < 1 || c->num_pages > 0x7fffffff) return MQ_ERR_SHAPE;
+    if (b->batch < 1 || b->batch > 1 << 20 || b->max_pages < 1 || b->max_pages > 0x7fffffff / c->page_size)
+        return MQ_ERR_SHAPE;
+    if (T < 1 || T > 1 << 24) return MQ_ERR_SHAPE;
+    if (q_heads < c->kv_heads || q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > 128) return MQ_ERR_SHAPE;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return MQ_ERR_ALIGN;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scales) | reinterpret_cast<uintptr_t>(c->v_scales) |
+                            reinterpret_cast<uintptr_t>(b->cu_rows) | reinterpret_cast<uintptr_t>(b->lens) |
+                            reinterpret_cast<uintptr_t>(b->page_table);
+    return words & 3u ? MQ_ERR_ALIGN : MQ_OK;
+}
+
+int mq_rope_kv_append(const void* qkv, int64_t T, int64_t row_stride, int32_t q_heads, const float* rope,
+                      int64_t max_pos, int32_t rot_dim, int32_t interleaved, const mq_kv_cache* cache,
+                      const mq_kv_batch* batch, void* q_out, void* ws, size_t ws_bytes, void* stream) {
+    if (!qkv || !q_out || (interleaved != 0 && interleaved != 1)) return MQ_ERR_INVALID_ARG;
+    int st = check_kv(cache, batch, T, q_heads);
+    if (st != MQ_OK) return st;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 != 0) return MQ_ERR_SHAPE;
+    if (rot_dim > 0 && (!rope || max_pos < 1)) return MQ_ERR_INVALID_ARG;
+    if (row_stride < (int64_t)(q_heads + 2 * cache->kv_heads) * cache->head_dim || row_stride % 8 != 0 ||
+        row_stride > (int64_t)1 << 32)
+        return MQ_ERR_SHAPE;
+    if (!aligned16(qkv) || !aligned16(q_out) || (rot_dim > 0 && !aligned16(rope))) return MQ_ERR_ALIGN;
+    int* status = nullptr;
+    if (ws) {
+        if (ws_bytes < mq::WS_HEADER_BYTES) return MQ_ERR_WORKSPACE;
+        if (!aligned16(ws)) return MQ_ERR_ALIGN;
+        status = static_cast<int*>(ws) + mq::WS_STATUS;
+    }
+    int sms = 0;
+    st = current_device_info(&sms);
+    if (st != MQ_OK) return st;
+    mq::KvAppendArgs a{qkv, T, row_stride, q_heads, rot_dim, interleaved, rope, max_pos, cache, batch, q_out, status};
+    return cuda_status(mq::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+static bool kv_attention_sizes_ok(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_q,
+                                  int64_t max_len) {
+    return batch >= 1 && batch <= 1 << 20 && kv_heads >= 1 && kv_heads <= 1024 && q_heads >= kv_heads &&
+           q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 && (head_dim == 64 || head_dim == 128) &&
+           max_q >= 1 && max_q <= 1 << 24 && max_len >= 0 && max_len <= 0x7fffffff;
+}
+
+size_t mq_kv_attention_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int64_t max_q, int64_t max_len) {
+    if (!kv_attention_sizes_ok(batch, q_heads, kv_heads, head_dim, max_q, max_len)) return 0;
+    return (size_t)mq::kv_plan(batch, q_heads, kv_heads, head_dim, max_q, max_len).bytes;
+}
+
+int mq_kv_attention(const void* q, int64_t T, int64_t q_row_stride, int32_t q_heads, const mq_kv_cache* cache,
+                    const mq_kv_batch* batch, int64_t max_q, int64_t max_len, float scale, void* out, void* ws,
+                    size_t ws_bytes, void* stream) {
+    if (!q || !out) return MQ_ERR_INVALID_ARG;
+    int st = check_kv(cache, batch, T, q_heads);
+    if (st != MQ_OK) return st;
+    if (!kv_attention_sizes_ok(batch->batch, q_heads, cache->kv_heads, cache->head_dim, max_q, max_len))
+        return MQ_ERR_SHAPE;
+    if (q_row_stride < (int64_t)q_heads * cache->head_dim || q_row_stride % 8 != 0 || q_row_stride > (int64_t)1 << 32)
+        return MQ_ERR_SHAPE;
+    if (!(scale > 0.f) || scale > 3.0e38f) return MQ_ERR_INVALID_ARG;
+    const mq::KvPlan plan =
+        mq::kv_plan(batch->batch, q_heads, cache->kv_heads, cache->head_dim, max_q, max_len);
+    if (plan.cells * plan.chunks > 0x7fffffff) return MQ_ERR_SHAPE;
+    if (!ws || ws_bytes < (size_t)plan.bytes) return MQ_ERR_WORKSPACE;
+    if (!aligned16(q) || !aligned16(out) || !aligned256(ws)) return MQ_ERR_ALIGN;
+    int sms = 0;
+    st = current_device_info(&sms);
+    if (st != MQ_OK) return st;
+    mq::KvAttentionArgs a{q, T, q_row_stride, q_heads, cache, batch, max_q, max_len, scale, out, ws};
+    return cuda_status(mq::launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
 int mq_debug_gemm_stall(const uint8_t* a_codes, const uint8_t* a_scales, const float* alpha_a,
                         const uint8_t* b_codes, const uint8_t* b_scales, const float* alpha_b, int64_t M, int64_t N,
                         int64_t K, void* y, void* ws, size_t ws_bytes, int64_t timeout_cycles, void* stream) {
@@ -415,9 +514,10 @@ int mq_debug_bounds_hits(int64_t* hits) {
     if (!hits) return MQ_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess) return MQ_ERR_CUDA;
     const unsigned long long q = mq::debug_hits_quant(), g = mq::gemm::debug_hits_gemm(),
-                             d = mq::decode::debug_hits_decode();
-    if (q == ~0ull || g == ~0ull || d == ~0ull) return MQ_ERR_CUDA;
-    *hits = (int64_t)(q + g + d);
+                             d = mq::decode::debug_hits_decode(), ka = mq::kv_append::debug_hits_kv_append(),
+                             kt = mq::kv_attend::debug_hits_kv_attend(), w = mq::w4a16::debug_hits_w4a16();
+    if (q == ~0ull || g == ~0ull || d == ~0ull || ka == ~0ull || kt == ~0ull || w == ~0ull) return MQ_ERR_CUDA;
+    *hits = (int64_t)(q + g + d + ka + kt + w);
     return MQ_OK;
 }
 

@@ -1,0 +1,45 @@
+// mq_kv_plan.h -- how mq_kv_attention splits a batch over the device: the rows
+// of a block, the chunks of a sequence's keys, and where its workspace holds
+// what.  A function of the call's sizes alone, so the workspace's size is too.
+#pragma once
+#include <algorithm>
+#include <cstdint>
+
+#include "mq_internal.h"
+
+namespace mq {
+
+struct KvPlan {
+    int nt;                   // n-tiles of 8 rows per block
+    int64_t row_tiles;        // tiles of rows (new token x head of the group) per (sequence, kv head)
+    int64_t cells;            // (sequence, row tile, kv head)
+    int64_t chunks;           // chunks of keys per cell at max_len
+    int64_t chunk_tokens;
+    int64_t tickets_off, part_off, bytes;
+};
+
+inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                      int64_t max_len) {
+    constexpr int64_t BLOCKS = 148 * 10;      // two waves of five blocks per SM
+    KvPlan p{};
+    const int64_t rows = max_q * (q_heads / kv_heads);
+    p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
+    p.cells = batch * p.row_tiles * kv_heads;
+    // one chunk where the cells fill the device; else enough chunks to do so,
+    // at most 64 (the last block to finish a cell reads them all) unless that
+    // makes them shorter than 1024 tokens
+    int64_t c = std::max<int64_t>(max_len, 64);
+    if (p.cells < BLOCKS)
+        c = std::max<int64_t>(64, std::min(std::max<int64_t>(1024, (max_len + 63) / 64),
+                                           (p.cells * max_len + BLOCKS - 1) / BLOCKS));
+    p.chunk_tokens = (c + 63) / 64 * 64;
+    p.chunks = std::max<int64_t>(1, (max_len + p.chunk_tokens - 1) / p.chunk_tokens);
+    // the tickets lie where they lie for every size, so a workspace serves calls of all sizes
+    p.tickets_off = (int64_t)WS_HEADER_BYTES;
+    p.part_off = p.tickets_off + BLOCKS * 4 / 256 * 256 + 256;
+    p.bytes = p.part_off + (p.chunks > 1 ? p.cells * p.chunks * 8 * p.nt * (head_dim + 2) * 4 : 0);
+    return p;
+}
+
+}  // namespace mq

@@ -25,6 +25,19 @@ MQ_ERR_TIMEOUT = -7
 _lib = None
 
 
+class _KVCache(ctypes.Structure):
+    """mq_kv_cache of mq.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _KVBatch(ctypes.Structure):
+    """mq_kv_batch of mq.h."""
+    _fields_ = [("cu_rows", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int64), ("batch", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class MQError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -58,6 +71,12 @@ def lib() -> ctypes.CDLL:
         L.mq_mlp_w4a4_workspace_bytes.argtypes = [i64, i64, i64]
         L.mq_mlp_w4a4_workspace_bytes.restype = sz
         L.mq_mlp_w4a4.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp, sz, vp]
+        i32, cache, batch = ctypes.c_int32, ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch)
+        L.mq_linear_w4a16.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp]
+        L.mq_rope_kv_append.argtypes = [vp, i64, i64, i32, vp, i64, i32, i32, cache, batch, vp, vp, sz, vp]
+        L.mq_kv_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i64]
+        L.mq_kv_attention_workspace_bytes.restype = sz
+        L.mq_kv_attention.argtypes = [vp, i64, i64, i32, cache, batch, i64, i64, ctypes.c_float, vp, vp, sz, vp]
         L.mq_is_debug_build.argtypes = []
         L.mq_debug_bounds_hits.argtypes = [ctypes.POINTER(ctypes.c_int64)]
         L.mq_set_switch.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -65,7 +84,7 @@ def lib() -> ctypes.CDLL:
         L.mq_debug_noalloc_fill_header.argtypes = [ctypes.c_uint32, vp]
         for name in ("mq_tensor_scale", "mq_tensor_amax", "mq_alpha_from_amax", "mq_nvfp4_quantize",
                      "mq_nvfp4_gemm", "mq_linear_w4a4", "mq_read_status", "mq_nvfp4_gemm_swiglu",
-                     "mq_mlp_w4a4", "mq_is_debug_build", "mq_debug_bounds_hits", "mq_set_switch",
+                     "mq_mlp_w4a4", "mq_linear_w4a16", "mq_rope_kv_append", "mq_kv_attention", "mq_is_debug_build", "mq_debug_bounds_hits", "mq_set_switch",
                      "mq_get_switch", "mq_debug_noalloc_fill_header"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -223,6 +242,130 @@ def mq_mlp_w4a4(x: torch.Tensor, wgu_codes, wgu_scales, alpha_gu, inter: int, wd
     _check(lib().mq_mlp_w4a4(_ptr(x), M, K, _ptr(wgu_codes), _ptr(wgu_scales), _ptr(alpha_gu), inter,
                              _ptr(wd_codes), _ptr(wd_scales), _ptr(alpha_d), N, _ptr(y), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream(stream)), "mq_mlp_w4a4")
+
+
+# The calls of a decode step are short, so their marshalling is too: one pass
+# of checks per tensor, addresses as plain integers.
+
+def _need(what: str, t: torch.Tensor, dtype, device) -> int:
+    """Address of a contiguous tensor of `dtype` on `device`."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous tensor expected")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor) -> torch.device:
+    """The tensor's device, which has to be the current one (the library
+    enqueues there)."""
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, but the current device is {torch.cuda.current_device()}")
+    return t.device
+
+
+def _stream_ptr(stream) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _row_stride(what: str, t: torch.Tensor, width: int) -> int:
+    """Elements between rows of a bf16 tensor [rows, ...] whose rows hold
+    `width` consecutive elements (rows may be apart)."""
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{what}: bfloat16 expected, got {t.dtype}")
+    if not (t.is_contiguous() or t[0].is_contiguous()):
+        raise ValueError(f"{what}: consecutive elements within a row expected")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def mq_linear_w4a16(x: torch.Tensor, w_codes, w_scales, alpha_w, N: int, y: torch.Tensor, stream=None) -> None:
+    """y = x W^T, x bf16 [M, K] with M <= 64, W quantized."""
+    dev = _device_of(x)
+    M, K = x.shape
+    if w_codes.numel() * w_codes.element_size() < N * K // 2:
+        raise ValueError("w_codes: smaller than an [N, K] weight's")
+    if w_scales.numel() * w_scales.element_size() < (N + 127) // 128 * 128 * ((K + 63) // 64 * 4):
+        raise ValueError("w_scales: smaller than an [N, K] weight's")
+    if y.numel() < M * N:
+        raise ValueError("y: smaller than [M, N]")
+    _check(lib().mq_linear_w4a16(_need("x", x, torch.bfloat16, dev), M, K,
+                                 _need("w_codes", w_codes, torch.uint8, dev),
+                                 _need("w_scales", w_scales, torch.uint8, dev),
+                                 _need("alpha_w", alpha_w, torch.float32, dev), N,
+                                 _need("y", y, torch.bfloat16, dev), _stream_ptr(stream)), "mq_linear_w4a16")
+
+
+def _kv_args(dev, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales):
+    """The mq_kv_cache and mq_kv_batch of a call's tensors."""
+    pages, heads, page, dim = k_codes.shape
+    codes = k_codes.dtype
+    if codes is not torch.float8_e4m3fn and codes is not torch.uint8:
+        raise ValueError(f"k_codes: float8_e4m3fn or uint8 expected, got {codes}")
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("v_codes: another shape than k_codes")
+    if k_scales.shape != (pages, heads) or v_scales.shape != (pages, heads):
+        raise ValueError("k_scales, v_scales: [pages, kv heads] expected")
+    batch, max_pages = page_table.shape
+    if cu_rows.numel() != batch + 1 or lens.numel() != batch:
+        raise ValueError("cu_rows [batch + 1], lens [batch] and page_table [batch, max_pages] do not agree")
+    i32, f32 = torch.int32, torch.float32
+    return (_KVCache(_need("k_codes", k_codes, codes, dev), _need("v_codes", v_codes, codes, dev),
+                     _need("k_scales", k_scales, f32, dev), _need("v_scales", v_scales, f32, dev),
+                     pages, page, heads, dim, 0),
+            _KVBatch(_need("cu_rows", cu_rows, i32, dev), _need("lens", lens, i32, dev),
+                     _need("page_table", page_table, i32, dev), max_pages, batch, 0))
+
+
+def mq_rope_kv_append(qkv: torch.Tensor, rope, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales,
+                      q_out: torch.Tensor, ws: torch.Tensor | None = None, rot_dim: int | None = None,
+                      interleaved: bool = False, stream=None) -> None:
+    """Rotates Q and K of qkv [T, (q heads + 2 kv heads) head_dim] into q_out
+    [T, q heads, head_dim] and, with V, into the cache (k_codes, v_codes
+    [pages, kv heads, page size, head_dim], scales [pages, kv heads]).  rope:
+    [positions, rot_dim] float32 (rope_table), None for rot_dim = 0."""
+    dev = _device_of(qkv)
+    cache, batch = _kv_args(dev, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales)
+    T, q_heads, dim = q_out.shape
+    width = (q_heads + 2 * cache.kv_heads) * cache.head_dim
+    if dim != cache.head_dim or qkv.dim() != 2 or tuple(qkv.shape) != (T, width):
+        raise ValueError("qkv [T, (q heads + 2 kv heads) head_dim] and q_out [T, q heads, head_dim] do not agree")
+    if rot_dim is None:
+        rot_dim = 0 if rope is None else rope.shape[1]
+    if rope is not None and (rope.dim() != 2 or rope.shape[1] != rot_dim):
+        raise ValueError("rope: [positions, rot_dim] expected")
+    _check(lib().mq_rope_kv_append(
+        qkv.data_ptr(), T, _row_stride("qkv", qkv, width), q_heads,
+        None if rope is None else _need("rope", rope, torch.float32, dev), 0 if rope is None else rope.shape[0],
+        rot_dim, 1 if interleaved else 0, cache, batch, _need("q_out", q_out, torch.bfloat16, dev),
+        None if ws is None else _need("ws", ws, torch.uint8, dev), 0 if ws is None else ws.numel(),
+        _stream_ptr(stream)), "mq_rope_kv_append")
+
+
+def mq_kv_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q: int,
+                                    max_len: int) -> int:
+    return int(lib().mq_kv_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim, max_q, max_len))
+
+
+def mq_kv_attention(q: torch.Tensor, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales,
+                    out: torch.Tensor, ws: torch.Tensor, max_q: int, max_len: int, scale: float,
+                    stream=None) -> None:
+    """Causal attention of q [T, q heads, head_dim] (rows may be apart, e.g. a
+    slice of a wider tensor) over the cache, into out of the same shape."""
+    dev = _device_of(q)
+    cache, batch = _kv_args(dev, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales)
+    T, q_heads, dim = q.shape
+    if dim != cache.head_dim or out.shape != q.shape or q.device != dev:
+        raise ValueError("q and out [T, q heads, head_dim] do not agree with the cache")
+    _check(lib().mq_kv_attention(q.data_ptr(), T, _row_stride("q", q, q_heads * dim), q_heads, cache, batch, max_q,
+                                 max_len, scale, _need("out", out, torch.bfloat16, dev),
+                                 _need("ws", ws, torch.uint8, dev), ws.numel(), _stream_ptr(stream)),
+           "mq_kv_attention")
 
 
 def mq_is_debug_build() -> bool:
