@@ -516,8 +516,10 @@ int mq_debug_bounds_hits(int64_t* hits) {
     const unsigned long long q = mq::debug_hits_quant(), g = mq::gemm::debug_hits_gemm(),
                              d = mq::decode::debug_hits_decode(), ka = mq::kv_append::debug_hits_kv_append(),
                              kt = mq::kv_attend::debug_hits_kv_attend(), w = mq::w4a16::debug_hits_w4a16();
-    if (q == ~0ull || g == ~0ull || d == ~0ull || ka == ~0ull || kt == ~0ull || w == ~0ull) return MQ_ERR_CUDA;
-    *hits = (int64_t)(q + g + d + ka + kt + w);
+    const unsigned long long kp = mq::kv_prefill::debug_hits_kv_prefill();
+    if (q == ~0ull || g == ~0ull || d == ~0ull || ka == ~0ull || kt == ~0ull || kp == ~0ull || w == ~0ull)
+        return MQ_ERR_CUDA;
+    *hits = (int64_t)(q + g + d + ka + kt + kp + w);
     return MQ_OK;
 }
 

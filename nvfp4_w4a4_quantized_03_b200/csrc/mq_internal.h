@@ -114,6 +114,8 @@ struct KvAttentionArgs {
     void* ws;
 };
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
+struct KvAttendParams;
+cudaError_t launch_kv_prefill(const KvAttendParams& p, int head_dim, int64_t blocks, cudaStream_t stream);
 
 // mq_linear_w4a16: M <= 64 rows of bf16 X against an NVFP4 weight.
 cudaError_t launch_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8_t* w_codes, const uint8_t* w_scales,
@@ -126,6 +128,7 @@ namespace gemm { unsigned long long debug_hits_gemm(); }
 namespace decode { unsigned long long debug_hits_decode(); }
 namespace kv_append { unsigned long long debug_hits_kv_append(); }
 namespace kv_attend { unsigned long long debug_hits_kv_attend(); }
+namespace kv_prefill { unsigned long long debug_hits_kv_prefill(); }
 namespace w4a16 { unsigned long long debug_hits_w4a16(); }
 
 // Readiness flags of the fused linear: one int per (128-row block, K stage).

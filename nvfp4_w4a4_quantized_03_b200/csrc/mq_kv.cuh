@@ -1,7 +1,12 @@
-// mq_kv.cuh -- what the append to the paged E4M3 cache and the attention over
-// it share: the page scale's range and its powers of two.
+// mq_kv.cuh -- what the append to the paged E4M3 cache and the two forms of the
+// attention over it share: the page scale's range, the attention's parameters,
+// and the join of a cell's chunks.
 #pragma once
 #include <cstdint>
+#include <cuda_bf16.h>
+
+#include "mq_debug.cuh"
+#include "mq_ptx.cuh"
 
 namespace mq {
 
@@ -11,5 +16,73 @@ namespace mq {
 constexpr int KV_E_MIN = -96, KV_E_MAX = 119;
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct KvAttendParams {
+    const __nv_bfloat16* q;              // [T, q_stride]
+    const int* cu;
+    const int* lens;
+    const int* table;
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const float* k_scales;
+    const float* v_scales;
+    __nv_bfloat16* out;                  // [T, q_heads, D]
+    int* status;
+    int* tickets;                        // one per (sequence, row tile, kv head)
+    float* part;                         // partial results
+    int64_t T, q_stride, num_pages, max_pages, max_len;
+    int batch, q_heads, kv_heads, group, page_log2, max_q;
+    int row_tiles, chunks, chunk_tokens;
+    float scale_log2;
+};
+
+// out of row `ri` (new token x head of the group) of the sequence at c0, four elements from 4 c4:
+// acc / lsum, zero for a row that saw nothing.
+template <int D>
+__device__ __forceinline__ void kv_write_out(const KvAttendParams& p, int c0, int64_t ri, int head, int c4,
+                                             const float4& acc, float lsum) {
+    const float inv = lsum > 0.f || lsum != lsum ? __fdiv_rn(1.f, lsum) : 0.f;
+    const int64_t at = ((c0 + ri / p.group) * p.q_heads + head * p.group + ri % p.group) * D + c4 * 4;
+    if (MQ_CHECK(at + 4 <= p.T * p.q_heads * (int64_t)D))
+        *reinterpret_cast<uint2*>(p.out + at) =
+            make_uint2(cvt_bf16x2(acc.y * inv, acc.x * inv), cvt_bf16x2(acc.w * inv, acc.z * inv));
+}
+
+// Joins a cell's chunks in their order: part is [chunk][rows_cap][D values, M, l].
+template <int D>
+__device__ __forceinline__ void kv_join(const KvAttendParams& p, const float* part, int chunks, int rows_cap,
+                                        int nrows, int c0, int64_t row0, int head, int tid, int threads) {
+    constexpr int V4 = D / 4;
+    const int64_t step = (int64_t)rows_cap * (D + 2);
+    for (int i = tid; i < nrows * V4; i += threads) {
+        const int r = i / V4, c4 = i % V4;
+        const float* src = part + (int64_t)r * (D + 2);
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int c = 0; c < chunks; ++c) top = fmaxf(top, __ldcg(src + c * step + D));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lsum = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < chunks; ++c) {
+            const float* pc = src + c * step;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + D));
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4));
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4 + 2));
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+            acc.x = __fmaf_rn(x.x, f, acc.x);
+            acc.y = __fmaf_rn(x.y, f, acc.y);
+            acc.z = __fmaf_rn(y.x, f, acc.z);
+            acc.w = __fmaf_rn(y.y, f, acc.w);
+            lsum = __fmaf_rn(ml.y, f, lsum);
+        }
+        kv_write_out<D>(p, c0, row0 + r, head, c4, acc, lsum);
+    }
+}
 
 }  // namespace mq

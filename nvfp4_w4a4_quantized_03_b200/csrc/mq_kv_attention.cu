@@ -44,24 +44,7 @@ constexpr int SEGMENT = 4096;            // tokens whose pages are held at a tim
 constexpr float LAZY = 8.f;              // M moves when a weight would pass 2^LAZY
 constexpr float BIAS = 6.f;              // weights are held times 2^BIAS: 2^14 at most, f16 holds 2^16
 
-struct Params {
-    const __nv_bfloat16* q;              // [T, q_stride]
-    const int* cu;
-    const int* lens;
-    const int* table;
-    const uint8_t* k_codes;
-    const uint8_t* v_codes;
-    const float* k_scales;
-    const float* v_scales;
-    __nv_bfloat16* out;                  // [T, q_heads, D]
-    int* status;
-    int* tickets;                        // one per (sequence, row tile, kv head)
-    float* part;                         // partial results
-    int64_t T, q_stride, num_pages, max_pages, max_len;
-    int batch, q_heads, kv_heads, group, page_log2, max_q;
-    int row_tiles, chunks, chunk_tokens;
-    float scale_log2;
-};
+using Params = KvAttendParams;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -73,11 +56,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float hi, float lo) {
     uint32_t r;
@@ -370,14 +348,6 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
     const int64_t cell = ((int64_t)b * p.row_tiles + tile) * p.kv_heads + head;
     float* part_ml = p.part ? p.part + cell * p.chunks * (int64_t)(ROWS * (D + 2)) : nullptr;
     const int nrows = last_row - row0 + 1;
-    auto write_out = [&](int r, int c4, float4 acc, float lsum) {
-        const float inv = lsum > 0.f || lsum != lsum ? __fdiv_rn(1.f, lsum) : 0.f;   // a row that sees nothing: zero
-        const int ri = row0 + r;
-        const int64_t at = ((int64_t)(c0 + ri / p.group) * p.q_heads + head * p.group + ri % p.group) * D + c4 * 4;
-        if (MQ_CHECK(at + 4 <= p.T * p.q_heads * (int64_t)D))
-            *reinterpret_cast<uint2*>(p.out + at) =
-                make_uint2(cvt_bf16x2(acc.y * inv, acc.x * inv), cvt_bf16x2(acc.w * inv, acc.z * inv));
-    };
     for (int i = tid; i < nrows * V4; i += THREADS) {
         const int r = i / V4, c4 = i % V4;
         float top = -INFINITY;
@@ -397,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
             lsum = __fmaf_rn(ll[w * ROWS + r], f, lsum);
         }
         if (chunks == 1) {
-            write_out(r, c4, acc, lsum);
+            kv_write_out<D>(p, c0, row0 + r, head, c4, acc, lsum);
         } else {
             // [chunk][row]: D values, M, l
             float* dst = part_ml + ((int64_t)chunk * ROWS + r) * (D + 2);
@@ -419,28 +389,7 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    for (int i = tid; i < nrows * V4; i += THREADS) {
-        const int r = i / V4, c4 = i % V4;
-        const float* src = part_ml + (int64_t)r * (D + 2);
-        float top = -INFINITY;
-        for (int c = 0; c < chunks; ++c) top = fmaxf(top, __ldcg(src + (int64_t)c * ROWS * (D + 2) + D));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < chunks; ++c) {
-            const float* pc = src + (int64_t)c * ROWS * (D + 2);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + D));
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4));
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4 + 2));
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-            acc.x = __fmaf_rn(x.x, f, acc.x);
-            acc.y = __fmaf_rn(x.y, f, acc.y);
-            acc.z = __fmaf_rn(y.x, f, acc.z);
-            acc.w = __fmaf_rn(y.y, f, acc.w);
-            lsum = __fmaf_rn(ml.y, f, lsum);
-        }
-        write_out(r, c4, acc, lsum);
-    }
+    kv_join<D>(p, part_ml, chunks, ROWS, nrows, c0, row0, head, tid, THREADS);
 }
 
 MQ_DEBUG_READER(debug_hits_kv_attend)
@@ -510,10 +459,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {
     p.scale_log2 = a.scale * 1.44269504088896340736f;
     const int64_t blocks = plan.cells * plan.chunks;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (plan.prefill) return launch_kv_prefill(p, c.head_dim, blocks, stream);
 #define MQ_KV_ATTEND(D_, NT_) \
     if (c.head_dim == D_ && plan.nt == NT_) return launch<D_, NT_>(p, blocks, stream);
-    MQ_KV_ATTEND(64, 1) MQ_KV_ATTEND(64, 2) MQ_KV_ATTEND(64, 4)
-    MQ_KV_ATTEND(128, 1) MQ_KV_ATTEND(128, 2) MQ_KV_ATTEND(128, 4)
+    MQ_KV_ATTEND(64, 1) MQ_KV_ATTEND(64, 2)
+    MQ_KV_ATTEND(128, 1) MQ_KV_ATTEND(128, 2)
 #undef MQ_KV_ATTEND
     return cudaErrorInvalidValue;
 }

@@ -10,7 +10,9 @@
 namespace mq {
 
 struct KvPlan {
-    int nt;                   // n-tiles of 8 rows per block
+    int nt;                   // n-tiles of 8 rows per block (form for few rows)
+    bool prefill;             // the tcgen05 form, 256 rows per block
+    int64_t block_rows;
     int64_t row_tiles;        // tiles of rows (new token x head of the group) per (sequence, kv head)
     int64_t cells;            // (sequence, row tile, kv head)
     int64_t chunks;           // chunks of keys per cell at max_len
@@ -20,25 +22,30 @@ struct KvPlan {
 
 inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
                       int64_t max_len) {
-    constexpr int64_t BLOCKS = 148 * 10;      // two waves of five blocks per SM
+    constexpr int64_t TICKETS = 148 * 10;
     KvPlan p{};
     const int64_t rows = max_q * (q_heads / kv_heads);
-    p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
+    p.prefill = rows > 16;
+    p.nt = p.prefill ? 0 : rows <= 8 ? 1 : 2;
+    p.block_rows = p.prefill ? 256 : 8 * p.nt;
+    p.row_tiles = (rows + p.block_rows - 1) / p.block_rows;
     p.cells = batch * p.row_tiles * kv_heads;
-    // one chunk where the cells fill the device; else enough chunks to do so,
-    // at most 64 (the last block to finish a cell reads them all) unless that
-    // makes them shorter than 1024 tokens
+    // one chunk where the cells fill the device (one block of the tcgen05 form
+    // per SM; two waves of five blocks of the other); else enough chunks to do
+    // so, at most 64 (the last block to finish a cell reads them all) unless
+    // that makes them shorter than 1024 tokens
+    const int64_t fill = p.prefill ? 148 : TICKETS;
     int64_t c = std::max<int64_t>(max_len, 64);
-    if (p.cells < BLOCKS)
-        c = std::max<int64_t>(64, std::min(std::max<int64_t>(1024, (max_len + 63) / 64),
-                                           (p.cells * max_len + BLOCKS - 1) / BLOCKS));
-    p.chunk_tokens = (c + 63) / 64 * 64;
+    if (p.cells < fill)
+        c = std::max<int64_t>(p.prefill ? 256 : 64, std::min(std::max<int64_t>(1024, (max_len + 63) / 64),
+                                                            (p.cells * max_len + fill - 1) / fill));
+    p.chunk_tokens = (c + 127) / 128 * 128;
+    if (!p.prefill) p.chunk_tokens = (c + 63) / 64 * 64;
     p.chunks = std::max<int64_t>(1, (max_len + p.chunk_tokens - 1) / p.chunk_tokens);
     // the tickets lie where they lie for every size, so a workspace serves calls of all sizes
     p.tickets_off = (int64_t)WS_HEADER_BYTES;
-    p.part_off = p.tickets_off + BLOCKS * 4 / 256 * 256 + 256;
-    p.bytes = p.part_off + (p.chunks > 1 ? p.cells * p.chunks * 8 * p.nt * (head_dim + 2) * 4 : 0);
+    p.part_off = p.tickets_off + TICKETS * 4 / 256 * 256 + 256;
+    p.bytes = p.part_off + (p.chunks > 1 ? p.cells * p.chunks * p.block_rows * (head_dim + 2) * 4 : 0);
     return p;
 }
 
