@@ -437,7 +437,8 @@ static bool kv_attention_sizes_ok(int32_t batch, int32_t q_heads, int32_t kv_hea
                                   int64_t max_len) {
     return batch >= 1 && batch <= 1 << 20 && kv_heads >= 1 && kv_heads <= 1024 && q_heads >= kv_heads &&
            q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 && (head_dim == 64 || head_dim == 128) &&
-           max_q >= 1 && max_q <= 1 << 24 && max_len >= 0 && max_len <= 0x7fffffff;
+           max_q >= 1 && max_q <= 1 << 24 && max_q * (q_heads / kv_heads) <= 0x7fff0000 && max_len >= 0 &&
+           max_len <= 0x7fff0000;
 }
 
 size_t mq_kv_attention_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,

@@ -15,17 +15,24 @@
 //                    the left operand of the second product
 //   warps 8-11       converters: E4M3 codes from global memory to f16 in shared
 //                    memory (128-byte swizzle), one block ahead in registers
+//   warp 13          looks up the pages and scales of the blocks to come
 //   warp 12          issues the products: S_t = Q_t K^T, then O_t += P_t V, the
 //                    two tiles alternating, so that one tile's softmax runs
 //                    under the other's products
 // V needs no transposition: [token][d] is the MN-major right operand.
 //
 // Bound: per block and CTA the two tiles' products take 2048 cycles of the
-// tensor pipe at D = 128, their 32768 exponentials 2048 cycles of the SFU, and
-// shared memory moves 256 KB, 2048 cycles: three resources near balance, so
-// the tensor pipe cannot be filled; figures beside launch_kv_prefill.
+// tensor pipe at D = 128 and their 32768 exponentials 2048 cycles of the SFU;
+// a tile's own chain (products 1420 cycles, scores and maximum 550, weights
+// 1750, hand-overs) is ~4000, and two tiles in turn leave either pipe about
+// half idle: 8192-token prompt, 32 heads of 128: 0.60 ms, 920 TFLOP/s.
+// Measured against this form and dropped: two threads per row (0.69 ms), the
+// weights under the last block's maximum, computed again where it rose (0.65
+// ms), a quarter of the exponentials as polynomials on the FMA pipe (no change).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "../../include/mq.h"
 #include "mq_debug.cuh"
@@ -41,16 +48,18 @@ constexpr int TILE = 128;                       // rows per tile
 constexpr int ROWS = 2 * TILE;
 constexpr int BLOCK = 128;                      // keys per block
 constexpr int GROUPS = BLOCK / 16;              // a page holds whole groups of 16 keys
-constexpr int CONV_WARP = 8, MMA_WARP = 12;
-constexpr int THREADS = 16 * 32;               // four warpgroups (warps 13-15 only hand back registers)
+constexpr int CONV_WARP = 8, MMA_WARP = 12, TABLE_WARP = 13;
+constexpr int THREADS = 16 * 32;               // four warpgroups (warps 14 and 15 only hand back registers)
 constexpr int STAGES = 2;                       // of K and of V
-constexpr int TABLES = 4;                       // of the blocks' page scales
+constexpr int TABLES = 4;                       // of the blocks' pages and their scales
 constexpr float LAZY = 8.f, BIAS = 6.f;         // as in mq_kv_attention.cu
+constexpr float FACTOR_MIN = 1.17549435e-38f;   // 2^-126
 constexpr long long TIMEOUT_CYCLES = 4000000000LL;
 
 struct Smem {
     uint64_t q_full, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
-    uint64_t s_full[2], p_full[2], o_full[2], t_full[TABLES], drained;
+    uint64_t s_full[2], p_full[2], o_full[2], t_full[TABLES], t_empty[TABLES], drained;
+    int64_t off[TABLES][GROUPS];                // byte offset of a group's codes in the pool, -1: none
     float ck[TABLES][GROUPS], ev[TABLES][GROUPS], iev[TABLES][GROUPS];
     uint32_t tmem_base;
     int abort_flag;
@@ -76,44 +85,78 @@ __device__ __forceinline__ uint32_t pack_f16(float hi, float lo) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// The products of one block, K = 16 per instruction, issued as one sequence:
+// operands by the low words of their shared-memory descriptors (in 16 bytes)
+// or their tensor-memory columns, the offsets of the steps as immediates, so
+// that the issuing lane keeps no table of descriptors.
+//   S = Q K^T: steps of 32 bytes inside the 128-byte swizzle row, then the next 64 d
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t hi) {
+#define MQ_STEP(off, p) \
+    "add.u32 ra, %1, " off ";\n\tadd.u32 rb, %2, " off ";\n\tmov.b64 da, {ra, %4};\n\tmov.b64 db, {rb, %4};\n\t" \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, " p ";\n\t"
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b32 ra, rb;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            MQ_STEP("0", "f") MQ_STEP("2", "t") MQ_STEP("4", "t") MQ_STEP("6", "t")
+            MQ_STEP("1024", "t") MQ_STEP("1026", "t") MQ_STEP("1028", "t") MQ_STEP("1030", "t")
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(hi) : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred f, t;\n\t.reg .b32 ra, rb;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            MQ_STEP("0", "f") MQ_STEP("2", "t") MQ_STEP("4", "t") MQ_STEP("6", "t")
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(hi) : "memory");
+    }
+#undef MQ_STEP
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+//   O (+)= P V: 8 columns of P and 16 tokens (2048 bytes) of V per step
+__device__ __forceinline__ void mma_outputs(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t hi, uint32_t acc) {
+#define MQ_STEP(aoff, boff, p) \
+    "add.u32 ra, %1, " aoff ";\n\tadd.u32 rb, %2, " boff ";\n\tmov.b64 db, {rb, %4};\n\t" \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], [ra], db, %3, " p ";\n\t"
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+        "{\n\t.reg .pred f, t;\n\t.reg .b32 ra, rb;\n\t.reg .b64 db;\n\tsetp.ne.b32 f, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        MQ_STEP("0", "0", "f") MQ_STEP("8", "128", "t") MQ_STEP("16", "256", "t") MQ_STEP("24", "384", "t")
+        MQ_STEP("32", "512", "t") MQ_STEP("40", "640", "t") MQ_STEP("48", "768", "t") MQ_STEP("56", "896", "t")
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(hi), "r"(acc) : "memory");
+#undef MQ_STEP
+}
+// ex2 that keeps its place among the other volatile instructions
+__device__ __forceinline__ float ex2v(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two binary32 operations per instruction
+__device__ __forceinline__ uint64_t pack2u(uint32_t x, uint32_t y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) { return pack2u(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
 }
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
     uint4 v;
     asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-// 16 codes -> 16 f16, two 16-byte stores
-__device__ __forceinline__ void store_f16(uint32_t addr, int chunk, int swz, int odd_first, const uint4& c) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[2 * i] = cvt_e4m3x2_to_f16x2((uint16_t)w[i]);
-        h[2 * i + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(w[i] >> 16));
-    }
-    // the two halves of a row are a multiple of 128 bytes apart: their lanes
-    // start with different chunks, so that a store meets no bank twice
-    const uint32_t a0 = addr + ((chunk ^ swz) << 4), a1 = addr + (((chunk + 1) ^ swz) << 4);
-    if (!odd_first) {
-        st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-        st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-    } else {
-        st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-        st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-    }
-}
-
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     using L = Layout<D>;
@@ -140,15 +183,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         if (tid == 0 && p.status) atomicExch(p.status, MQ_ERR_INVALID_ARG);
         return;
     }
-    const int64_t rows = (int64_t)n * p.group, row0 = (int64_t)tile * ROWS;
+    // positions and rows stay below 2^31 - 2^16 (checked by the entry point)
+    const int rows = n * p.group, row0 = tile * ROWS;
     if (row0 >= rows) return;
-    const int64_t start = len - n;
-    const int64_t last_row = min(rows, row0 + ROWS) - 1;
-    const int64_t end = max((int64_t)0, min(len, start + last_row / p.group + 1));
-    const int chunks = max(1, (int)((end + p.chunk_tokens - 1) / p.chunk_tokens));
+    const int start = (int)len - n;
+    const int last_row = min(rows, row0 + ROWS) - 1;
+    const int end = max(0, min((int)len, start + last_row / p.group + 1));
+    const int chunks = max(1, (int)(((int64_t)end + p.chunk_tokens - 1) / p.chunk_tokens));
     if (chunk >= chunks) return;
-    const int64_t k0 = (int64_t)chunk * p.chunk_tokens, k1 = min(end, k0 + p.chunk_tokens);
-    const int blocks = k1 > k0 ? (int)((k1 - k0 + BLOCK - 1) / BLOCK) : 0;
+    const int k0 = chunk * p.chunk_tokens, k1 = (int)min((int64_t)end, (int64_t)k0 + p.chunk_tokens);
+    const int blocks = k1 > k0 ? (k1 - k0 + BLOCK - 1) / BLOCK : 0;
     const bool two = row0 + TILE < rows;                     // the second tile has rows
 
     if (tid == 0) {
@@ -159,7 +203,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
             mbar_init(&s->k_empty[i], 1);
             mbar_init(&s->v_empty[i], 1);
         }
-        for (int i = 0; i < TABLES; ++i) mbar_init(&s->t_full[i], 1);
+        for (int i = 0; i < TABLES; ++i) {
+            mbar_init(&s->t_full[i], 1);
+            mbar_init(&s->t_empty[i], two ? 12 : 8);
+        }
         mbar_init(&s->drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->s_full[i], 1);
@@ -191,13 +238,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     };
 
     // 512 threads start with 128 registers each; the softmax warpgroups take
-    // what the others leave: 2 x 176 + 96 + 64 = 4 x 128
+    // what the others leave: 2 x 176 + 80 + 80 = 4 x 128
     if (warp < CONV_WARP)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else if (warp < MMA_WARP)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
 
     float m = -INFINITY, l = 0.f;                            // softmax threads: their row's
     if (blocks == 0) {
@@ -206,10 +253,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         // ------------------------------------------------------------ softmax
         const int t = warp / 4;                              // tile
         const int r = tid % TILE;                            // row of the tile
-        const int64_t row = row0 + t * TILE + r;
+        const int row = row0 + t * TILE + r;
         const bool mine = row < rows;
         float fac = 0.f;
-        int64_t pos = -1;
+        int pos = -1;
         {
             uint4 w[D / 8];
             float top = 0.f;
@@ -217,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
             for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0, 0, 0, 0);
             if (mine) {
                 pos = start + row / p.group;
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (c0 + row / p.group) * p.q_stride +
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(c0 + row / p.group) * p.q_stride +
                                                                   (head * p.group + row % p.group) * D);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) w[i] = src[i];
@@ -249,83 +296,126 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + L::S_COL + t * BLOCK;
         const uint32_t o_addr = tmem + lanes + L::O_COL + t * D;
-        const int64_t sees_all = start + (row0 + t * TILE) / p.group;     // keys every row of the tile sees
+        const int sees_all = start + (row0 + t * TILE) / p.group;     // keys every row of the tile sees
         if (t == 0 || two) {
             for (int j = 0; j < blocks; ++j) {
-                const int64_t kb = k0 + (int64_t)j * BLOCK;
+                const int kb = k0 + j * BLOCK;
                 if (!wait(&s->t_full[j % TABLES], (j / TABLES) & 1) || !wait(&s->s_full[t], j & 1)) break;
                 tc_fence_after();
-                const float* ck = s->ck[j % TABLES];
-                const float* ev = s->ev[j % TABLES];
-                const float* iev = s->iev[j % TABLES];
                 const bool masked = kb + BLOCK - 1 > min(sees_all, k1 - 1);
-                const int limit = (int)min((int64_t)BLOCK, min(pos, k1 - 1) - kb);   // last key of the block it sees
-                float top = -INFINITY;
+                if (masked) {
+                    const int limit = min(pos, k1 - 1) - kb;     // last key of the block the row sees
 #pragma unroll
-                for (int c = 0; c < BLOCK; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(s_addr + c, v);
-                    tmem_ld_wait_regs(v);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float gm = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float x = __uint_as_float(v[g * 16 + i]);
-                            if (masked) x = c + g * 16 + i <= limit ? x : -INFINITY;
-                            gm = fmaxf(gm, x);
-                        }
-                        // -inf stays -inf where the factor is 0 (an empty row of Q has fac > 0 all the same)
-                        const float u = __fmaf_rn(gm, fac * ck[c / 16 + g], ev[c / 16 + g]);
-                        top = fmaxf(top, gm == -INFINITY ? -INFINITY : u);
-                    }
-                }
-                float f = 1.f;
-                if (top > m + LAZY) {
-                    f = ex2(m - top);
-                    m = top;
-                    l *= f;
-                }
-                if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c = 0; c < BLOCK; c += 32) {
                         uint32_t v[32];
-                        tmem_ld_32x32b_x32(o_addr + c, v);
+                        tmem_ld_32x32b_x32(s_addr + c, v);
                         tmem_ld_wait_regs(v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                        tmem_st_32x32b_x32(o_addr + c, v);
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i > limit) v[i] = 0xFF800000u;                        // -inf
+                        tmem_st_32x32b_x32(s_addr + c, v);
+                    }
+                    tmem_st_wait();
+                }
+                // the block's maximum
+                float top = -INFINITY, fck[GROUPS], sh[GROUPS], iev[GROUPS];
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    // a factor of 0 would make NaN of -inf: it underflows only where the scores are 0 all the same
+                    fck[g] = fmaxf(fac * s->ck[j % TABLES][g], FACTOR_MIN);
+                    sh[g] = s->ev[j % TABLES][g];
+                    iev[g] = s->iev[j % TABLES][g];
+                }
+                {
+                    uint32_t v[2][32];
+                    tmem_ld_32x32b_x32(s_addr, v[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait_regs(v[c & 1]);
+                        if (c < 3) tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[1 - (c & 1)]);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint32_t* x = v[c & 1] + 16 * g;
+                            float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
+#pragma unroll
+                            for (int i = 6; i < 14; i += 4) {
+                                g0 = max3(__float_as_uint(g0), x[i], x[i + 1]);
+                                g1 = max3(__float_as_uint(g1), x[i + 2], x[i + 3]);
+                            }
+                            g0 = fmaxf(max3(__float_as_uint(g0), x[14], x[15]), g1);
+                            top = fmaxf(top, __fmaf_rn(g0, fck[2 * c + g], sh[2 * c + g]));
+                        }
                     }
                 }
-                const float shift = BIAS - (m == -INFINITY ? 0.f : m);
+                if (__any_sync(0xffffffffu, top > m + LAZY)) {
+                    const float f = top > m + LAZY ? ex2(m - top) : 1.f;
+                    if (top > m + LAZY) m = top;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_addr + c, o);
+                            tmem_ld_wait_regs16(o);
 #pragma unroll
-                for (int c = 0; c < BLOCK; c += 32) {
-                    uint32_t v[32], h[16];
-                    tmem_ld_32x32b_x32(s_addr + c, v);
-                    tmem_ld_wait_regs(v);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float fck = fac * ck[c / 16 + g], sh = ev[c / 16 + g] + shift;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float x = ex2(__fmaf_rn(__uint_as_float(v[g * 16 + i]), fck, sh));
-                            float y = ex2(__fmaf_rn(__uint_as_float(v[g * 16 + i + 1]), fck, sh));
-                            if (masked) {
-                                x = c + g * 16 + i <= limit ? x : 0.f;
-                                y = c + g * 16 + i + 1 <= limit ? y : 0.f;
-                            }
-                            sum += x + y;
-                            h[g * 8 + i / 2] = pack_f16(y, x);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st_32x32b_x16(o_addr + c, o);
                         }
-                        l = __fmaf_rn(sum, iev[c / 16 + g], l);
                     }
-                    tmem_st_32x32b_x16(s_addr + c / 2, h);
+                }
+                // The weights, group by group: the exponentials of one beside
+                // the sums and conversions of the one before (a result of the
+                // SFU that is needed at once stalls the warp: 2514 -> 1329
+                // cycles per 128 keys of a lone warp).
+                const float shift = BIAS - (m == -INFINITY ? 0.f : m);
+                uint32_t v[2][16];
+                uint64_t u[2][8];
+                float e[2][16];
+                auto exponents = [&](int g) {
+                    const uint32_t* x = v[g & 1];
+                    tmem_ld_wait_regs16(v[g & 1]);
+                    if (g + 1 < GROUPS) tmem_ld_32x32b_x16(s_addr + 16 * (g + 1), v[1 - (g & 1)]);
+                    const uint64_t fck2 = pack2(fck[g], fck[g]), sh2 = pack2(sh[g] + shift, sh[g] + shift);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[g & 1][i] = fma2(pack2u(x[2 * i], x[2 * i + 1]), fck2, sh2);
+                };
+                tmem_ld_32x32b_x16(s_addr, v[0]);
+                exponents(0);
+#pragma unroll
+                for (int g = 0; g <= GROUPS; ++g) {
+                    if (g < GROUPS) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float w0, w1;
+                            unpack2(u[g & 1][i], w0, w1);
+                            e[g & 1][2 * i] = ex2v(w0);
+                            e[g & 1][2 * i + 1] = ex2v(w1);
+                        }
+                        if (g + 1 < GROUPS) exponents(g + 1);
+                    }
+                    if (g > 0) {
+                        const float* w = e[1 - (g & 1)];
+                        uint64_t sum = pack2(w[0], w[1]);
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (i > 0) sum = add2(sum, pack2(w[2 * i], w[2 * i + 1]));
+                            h[i] = pack_f16(w[2 * i + 1], w[2 * i]);
+                        }
+                        float w0, w1;
+                        unpack2(sum, w0, w1);
+                        l = __fmaf_rn(w0 + w1, iev[g - 1], l);
+                        // group g - 1's weights lie over scores of groups that were read before
+                        tmem_st_32x32b_x8(s_addr + 8 * (g - 1), h);
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->p_full[t]);
+                if (lane == 0) {
+                    mbar_arrive(&s->p_full[t]);
+                    mbar_arrive(&s->t_empty[j % TABLES]);
+                }
             }
         }
     } else if (warp < MMA_WARP) {
@@ -333,85 +423,109 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         constexpr int PIECES = D / 16;                       // 16-byte pieces of a token
         constexpr int TOKENS = 128 / PIECES;                 // tokens per pass of the 128 threads
         constexpr int PASSES = BLOCK / TOKENS;
+        // Thread -> (token, piece): eight consecutive threads store four pieces
+        // of two neighbouring tokens, whose swizzles differ in the lowest bit,
+        // so a 16-byte store of theirs meets every bank once.
         const int i = tid - CONV_WARP * 32;
-        const int piece = i % PIECES, tok = i / PIECES;
-        const uint32_t half = (piece >> 2) * (BLOCK * 128);
-        const int chunk16 = (piece & 3) * 2;
-        const int odd = piece >> 2;
-        const int64_t head_bytes = (int64_t)page_tokens * D;
-        [[maybe_unused]] const int64_t pool = p.num_pages * p.kv_heads * head_bytes;
-        // lane g of each warp: group g of a block, its byte offset in the pool (-1: nothing to read)
-        int64_t off = -1;
-        float gk = 0.f, gv = 1.f;
-        auto find = [&](int j) {
-            off = -1;
-            gk = 0.f;
-            gv = 1.f;
-            const int64_t at = k0 + (int64_t)j * BLOCK + lane * 16;
-            if (lane < GROUPS && j < blocks && at < k1) {
+        const int piece = D == 64 ? i & 3 : (i & 3) | (i >> 1 & 4);
+        const int tok = D == 64 ? i >> 2 : (i >> 2 & 1) | (i >> 3 & 14);
+        const uint32_t row = (piece >> 2) * (BLOCK * 128) + tok * 128;
+        const uint32_t at0 = row + ((((piece & 3) * 2) ^ (tok & 7)) << 4);
+        const uint32_t at1 = row + ((((piece & 3) * 2 + 1) ^ (tok & 7)) << 4);
+        const int within = (tok & 15) * D + piece * 16;
+        [[maybe_unused]] const int64_t pool = (p.num_pages * p.kv_heads << p.page_log2) * D;
+        uint4 kc[PASSES], vc[PASSES];
+        auto load = [&](uint4 (&c)[PASSES], const uint8_t* codes, int j) {
+            const int64_t* off = s->off[j % TABLES];
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+                const int64_t o = max(off[q * TOKENS / 16 + (TOKENS == 32 ? tok >> 4 : 0)], (int64_t)0) + within;
+                c[q] = make_uint4(0, 0, 0, 0);
+                if (MQ_CHECK(o + 16 <= pool)) c[q] = load_codes(codes + o);
+            }
+            // behind the last key a page holds whatever was there, a NaN code
+            // times a zero weight is no zero: zeros instead
+            const int left = k1 - (k0 + j * BLOCK);
+            if (left < BLOCK) {
+#pragma unroll
+                for (int q = 0; q < PASSES; ++q)
+                    if (q * TOKENS + tok >= left) c[q] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto store = [&](uint32_t dst, const uint4 (&c)[PASSES]) {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+                const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[2 * e] = cvt_e4m3x2_to_f16x2((uint16_t)w[e]);
+                    h[2 * e + 1] = cvt_e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
+                }
+                st_shared_v4(dst + at0 + q * TOKENS * 128, h[0], h[1], h[2], h[3]);
+                st_shared_v4(dst + at1 + q * TOKENS * 128, h[4], h[5], h[6], h[7]);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+        };
+        bool ok = wait(&s->t_full[0], 0);
+        if (ok) {
+            load(kc, p.k_codes, 0);
+            load(vc, p.v_codes, 0);
+            if (lane == 0) mbar_arrive(&s->t_empty[0]);
+        }
+        for (int j = 0; ok && j < blocks; ++j) {
+            const int st = j % STAGES, nt = (j + 1) % TABLES;
+            const uint32_t phase = (j / STAGES) & 1;
+            const bool more = j + 1 < blocks;
+            ok = wait(&s->k_empty[st], phase ^ 1);
+            if (!ok) break;
+            store(sbase + L::K_OFF + st * L::TILE_BYTES, kc);
+            if (lane == 0) mbar_arrive(&s->k_full[st]);
+            if (more) {
+                ok = wait(&s->t_full[nt], ((j + 1) / TABLES) & 1);
+                if (!ok) break;
+                load(kc, p.k_codes, j + 1);
+            }
+            ok = wait(&s->v_empty[st], phase ^ 1);
+            if (!ok) break;
+            store(sbase + L::V_OFF + st * L::TILE_BYTES, vc);
+            if (lane == 0) mbar_arrive(&s->v_full[st]);
+            if (more) {
+                load(vc, p.v_codes, j + 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->t_empty[nt]);
+            }
+        }
+    } else if (warp == TABLE_WARP) {
+        // ------------------------------------------------------------ tables
+        // of the blocks to come: lane g looks up group g
+        for (int j = 0; j < blocks; ++j) {
+            const int tb = j % TABLES;
+            int64_t off = -1;
+            float gk = 0.f, gv = 1.f;
+            const int at = k0 + j * BLOCK + lane * 16;
+            if (lane < GROUPS && at < k1) {
                 const int64_t page = p.table[(int64_t)b * p.max_pages + (at >> p.page_log2)];
                 if (page >= 0 && page < p.num_pages) {
                     const int64_t cell = page * p.kv_heads + head;
-                    off = cell * head_bytes + (at & (page_tokens - 1)) * D;
+                    off = ((cell << p.page_log2) + (at & (page_tokens - 1))) * D;
                     gk = p.k_scales[cell];
                     gv = p.v_scales[cell];
                 } else if (p.status) {
                     atomicExch(p.status, MQ_ERR_INVALID_ARG);
                 }
             }
-        };
-        uint4 kc[PASSES], vc[PASSES];
-        auto load = [&](uint4 (&c)[PASSES], const uint8_t* codes, int64_t o, int j) {
-#pragma unroll
-            for (int q = 0; q < PASSES; ++q) {
-                const int token = q * TOKENS + tok;
-                const int64_t go = __shfl_sync(0xffffffffu, o, token >> 4);
-                const int64_t at = go + (token & 15) * D + piece * 16;
-                c[q] = make_uint4(0, 0, 0, 0);
-                // behind the last key a page holds whatever was there: zeros instead
-                if (go >= 0 && k0 + (int64_t)j * BLOCK + token < k1 && MQ_CHECK(at + 16 <= pool)) c[q] = load_codes(codes + at);
-            }
-        };
-        find(0);
-        load(kc, p.k_codes, off, 0);
-        load(vc, p.v_codes, off, 0);
-        for (int j = 0; j < blocks; ++j) {
-            const int st = j % STAGES;
-            const uint32_t phase = (j / STAGES) & 1;
-            if (!wait(&s->k_empty[st], phase ^ 1)) break;
-            // The block's scales.  Table j % 4 is free: the stage just freed was
-            // block j - 2's, whose scores needed both tiles' weights of block j - 3.
-            if (warp == CONV_WARP) {
-                if (lane < GROUPS) {
-                    s->ck[j % TABLES][lane] = gk;
-                    s->ev[j % TABLES][lane] = (float)((int)(__float_as_uint(gv) >> 23) - 127);
-                    s->iev[j % TABLES][lane] = __uint_as_float((254u << 23) - (__float_as_uint(gv) & 0x7F800000u));
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->t_full[j % TABLES]);
-            }
-            find(j + 1);
-            const uint32_t kdst = sbase + L::K_OFF + st * L::TILE_BYTES + half;
-#pragma unroll
-            for (int q = 0; q < PASSES; ++q) {
-                const int token = q * TOKENS + tok;
-                store_f16(kdst + token * 128, chunk16, token & 7, odd, kc[q]);
-            }
-            fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s->k_full[st]);
-            if (j + 1 < blocks) load(kc, p.k_codes, off, j + 1);
-            if (!wait(&s->v_empty[st], phase ^ 1)) break;
-            const uint32_t vdst = sbase + L::V_OFF + st * L::TILE_BYTES + half;
-#pragma unroll
-            for (int q = 0; q < PASSES; ++q) {
-                const int token = q * TOKENS + tok;
-                store_f16(vdst + token * 128, chunk16, token & 7, odd, vc[q]);
+            if (!wait(&s->t_empty[tb], ((j / TABLES) & 1) ^ 1)) break;
+            if (lane < GROUPS) {
+                s->off[tb][lane] = off;
+                s->ck[tb][lane] = gk;
+                s->ev[tb][lane] = (float)((int)(__float_as_uint(gv) >> 23) - 127);
+                s->iev[tb][lane] = __uint_as_float((254u << 23) - (__float_as_uint(gv) & 0x7F800000u));
             }
-            fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s->v_full[st]);
-            if (j + 1 < blocks) load(vc, p.v_codes, off, j + 1);
+            if (lane == 0) mbar_arrive(&s->t_full[tb]);
         }
     } else if (warp == MMA_WARP) {
         // ------------------------------------------------------------ products
@@ -420,27 +534,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         constexpr uint32_t ID_S = (1u << 4) | ((uint32_t)(BLOCK >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
         constexpr uint32_t ID_O = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
         const bool leader = elect_one();
+        // high words of the descriptors: 1024 bytes between groups of 8 rows,
+        // version 1, 128-byte swizzle; V's low word also holds the 16 KB between
+        // its halves of 64 d
+        constexpr uint32_t HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+        const uint32_t q_lo = ((sbase + L::Q_OFF) >> 4 & 0x3FFF) | 1u << 16, k_lo = ((sbase + L::K_OFF) >> 4 & 0x3FFF) | 1u << 16;
+        const uint32_t v_lo = ((sbase + L::V_OFF) >> 4 & 0x3FFF) | (uint32_t)(BLOCK * 128 >> 4) << 16;
         auto scores = [&](int t, int st) {
-            const uint64_t a = smem_desc(sbase + L::Q_OFF + t * L::TILE_BYTES, 16, 1024, 2);
-            const uint64_t bd = smem_desc(sbase + L::K_OFF + st * L::TILE_BYTES, 16, 1024, 2);
             if (leader) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t step = (uint64_t)((k / 4) * (TILE * 128) + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + L::S_COL + t * BLOCK, a + step, bd + step, ID_S, k != 0);
-                }
+                mma_scores<D>(tmem + L::S_COL + t * BLOCK, q_lo + t * (L::TILE_BYTES >> 4), k_lo + st * (L::TILE_BYTES >> 4), ID_S, HI);
                 mma_commit(&s->s_full[t]);
             }
             __syncwarp();
         };
         auto outputs = [&](int t, int st, bool first) {
-            const uint64_t bd = smem_desc(sbase + L::V_OFF + st * L::TILE_BYTES, BLOCK * 128, 1024, 2);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < BLOCK / 16; ++k)
-                    mma_ts(tmem + L::O_COL + t * D, tmem + L::S_COL + t * BLOCK + k * 8, bd + (uint64_t)(k * 2048 >> 4),
-                           ID_O, !(first && k == 0));
-            }
+            if (leader)
+                mma_outputs(tmem + L::O_COL + t * D, tmem + L::S_COL + t * BLOCK, v_lo + st * (L::TILE_BYTES >> 4), ID_O, HI, !first);
             __syncwarp();
         };
         auto run = [&]() {
@@ -486,12 +595,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     float* part = p.part ? p.part + cell * p.chunks * (int64_t)(ROWS * (D + 2)) : nullptr;
     if (warp < CONV_WARP && !(warp >= 4 && !two)) {
         const int t = warp / 4;
-        const int64_t row = row0 + tid;                      // tid = 128 t + row of the tile
+        const int row = row0 + tid;                          // tid = 128 t + row of the tile
         const uint32_t o_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::O_COL + t * D;
         const bool have = blocks > 0 && wait(&s->o_full[t], 0);
         tc_fence_after();
         const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;       // a row that sees nothing: zero
-        const int64_t at = ((c0 + row / p.group) * p.q_heads + head * p.group + row % p.group) * D;
+        const int64_t at = ((int64_t)(c0 + row / p.group) * p.q_heads + head * p.group + row % p.group) * D;
         float* dst = part ? part + ((int64_t)chunk * ROWS + tid) * (D + 2) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -545,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     __syncthreads();
     if (!s->last) return;
     __threadfence();
-    kv_join<D>(p, part, chunks, ROWS, (int)(last_row - row0 + 1), c0, row0, head, tid, THREADS);
+    kv_join<D>(p, part, chunks, ROWS, last_row - row0 + 1, c0, row0, head, tid, THREADS);
 }
 
 MQ_DEBUG_READER(debug_hits_kv_prefill)
