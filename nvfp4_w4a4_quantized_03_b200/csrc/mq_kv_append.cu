@@ -30,6 +30,8 @@
 namespace mq {
 namespace kv_append {
 
+constexpr int Q_ROWS = 2;                 // rows of Q per block
+
 struct Params {
     const __nv_bfloat16* qkv;     // [T, row_stride]
     const float* rope;            // [max_pos, rot_dim], cosines then sines
@@ -45,7 +47,6 @@ struct Params {
     int64_t T, row_stride, max_pos, num_pages, max_pages;
     int batch, q_heads, kv_heads, rot_dim, interleaved;
     int kv_blocks;                // blocks [0, kv_blocks) append, the rest rotate Q
-    int q_rows;                   // rows of Q per block
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
@@ -136,9 +137,9 @@ __device__ __forceinline__ void decode8(const uint2& v, float (&x)[8]) {
 template <int D, int P>
 struct Shape {
     static constexpr int LANES = D / 8;
-    static constexpr int THREADS = P * LANES < 256 ? P * LANES : 256;
-    static constexpr int TOKENS = THREADS / LANES;       // per pass
-    static constexpr int PASSES = P / TOKENS;
+    static constexpr int PASSES = P * LANES >= 256 ? 2 : 1;
+    static constexpr int THREADS = P * LANES / PASSES;
+    static constexpr int TOKENS = P / PASSES;            // per pass
     static_assert(TOKENS * PASSES == P && THREADS % 32 == 0, "page shape");
 };
 
@@ -147,7 +148,7 @@ template <int D, int P>
 __device__ __forceinline__ void append_page(const Params& p, int block) {
     using S = Shape<D, P>;
     __shared__ int s_seq;
-    __shared__ uint32_t s_top[2][8];
+    __shared__ uint32_t s_top[2][32];
     const int tid = threadIdx.x;
     const int slot = block / p.kv_heads, head = block % p.kv_heads;
     // Slots of sequence b start at cu[b] / P + 2 b: its n new tokens touch at
@@ -284,20 +285,19 @@ __device__ __forceinline__ void append_page(const Params& p, int block) {
     }
 }
 
-// `q_rows` rows of Q: a thread keeps 8 columns, so a row's cosines and sines
-// are loaded once for all the heads it walks.
+// Two rows of Q: a thread keeps 8 columns of one head at a time, the loads of
+// both rows in flight together.
 template <int D>
 __device__ __forceinline__ void rotate_q(const Params& p, int block, int threads) {
     constexpr int LANES = D / 8;
-    __shared__ int64_t s_pos[8];
+    __shared__ int64_t s_pos[Q_ROWS];
     const int tid = threadIdx.x;
-    const int64_t r0 = (int64_t)block * p.q_rows;
-    const int rows = (int)min((int64_t)p.q_rows, p.T - r0);
-    if (tid < 8) s_pos[tid] = -1;
+    const int64_t r0 = (int64_t)block * Q_ROWS;
+    if (tid < Q_ROWS) s_pos[tid] = -1;
     __syncthreads();
     for (int b = tid; b < p.batch; b += threads) {
         const int64_t c0 = p.cu[b], c1 = p.cu[b + 1];
-        const int64_t lo = max(c0, r0), hi = min(c1, r0 + rows);
+        const int64_t lo = max(c0, r0), hi = min(min(c1, r0 + Q_ROWS), p.T);
         if (lo < hi) {
             const int64_t shift = (int64_t)p.lens[b] - c1;
             for (int64_t r = lo; r < hi; ++r) s_pos[r - r0] = r + shift;
@@ -307,36 +307,46 @@ __device__ __forceinline__ void rotate_q(const Params& p, int block, int threads
     const int lane = tid % LANES, d0 = lane * 8, groups = threads / LANES;
     const bool rotated = d0 < p.rot_dim;
     const int partner = !p.interleaved && rotated ? partner_offset(d0, p.rot_dim) : 0;
-    for (int r = 0; r < rows; ++r) {
-        const int64_t pos = s_pos[r];
-        if (pos < 0) continue;                    // padding: the row stays as it was
-        if (rotated && pos >= p.max_pos) {
+    int64_t pos[Q_ROWS];
+#pragma unroll
+    for (int r = 0; r < Q_ROWS; ++r) {
+        pos[r] = s_pos[r];                        // negative: padding, the row stays as it was
+        if (rotated && pos[r] >= p.max_pos) {
             if (p.status) atomicExch(p.status, MQ_ERR_INVALID_ARG);
-            continue;
+            pos[r] = -1;
         }
-        CosSin cs;
-        if (rotated) load_cos_sin(p.rope + pos * p.rot_dim, d0, p.rot_dim, p.interleaved, cs);
-        const __nv_bfloat16* src = p.qkv + (r0 + r) * p.row_stride + d0;
-        __nv_bfloat16* dst = p.q_out + (r0 + r) * (int64_t)p.q_heads * D + d0;
-#pragma unroll 4
-        for (int h = tid / LANES; h < p.q_heads; h += groups) {
-            uint4 w = *reinterpret_cast<const uint4*>(src + h * D);
-            if (rotated) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (partner) y = *reinterpret_cast<const uint4*>(src + h * D + partner);
-                float x[8];
-                unpack8(w, x);
-                rotate8(x, y, d0, p.rot_dim, p.interleaved, cs);
-                w = make_uint4(cvt_bf16x2(x[1], x[0]), cvt_bf16x2(x[3], x[2]), cvt_bf16x2(x[5], x[4]),
-                               cvt_bf16x2(x[7], x[6]));
+    }
+    for (int h = tid / LANES; h < p.q_heads; h += groups) {
+        const __nv_bfloat16* src = p.qkv + r0 * p.row_stride + h * D + d0;
+        uint4 w[Q_ROWS], y[Q_ROWS];
+#pragma unroll
+        for (int r = 0; r < Q_ROWS; ++r) {
+            w[r] = y[r] = make_uint4(0, 0, 0, 0);
+            if (pos[r] >= 0) {
+                w[r] = *reinterpret_cast<const uint4*>(src + r * p.row_stride);
+                if (partner) y[r] = *reinterpret_cast<const uint4*>(src + r * p.row_stride + partner);
             }
-            if (MQ_CHECK(r0 + r < p.T && h < p.q_heads)) *reinterpret_cast<uint4*>(dst + h * D) = w;
+        }
+#pragma unroll
+        for (int r = 0; r < Q_ROWS; ++r) {
+            if (pos[r] < 0) continue;
+            if (rotated) {
+                CosSin cs;
+                load_cos_sin(p.rope + pos[r] * p.rot_dim, d0, p.rot_dim, p.interleaved, cs);
+                float x[8];
+                unpack8(w[r], x);
+                rotate8(x, y[r], d0, p.rot_dim, p.interleaved, cs);
+                w[r] = make_uint4(cvt_bf16x2(x[1], x[0]), cvt_bf16x2(x[3], x[2]), cvt_bf16x2(x[5], x[4]),
+                                  cvt_bf16x2(x[7], x[6]));
+            }
+            if (MQ_CHECK(r0 + r < p.T && h < p.q_heads))
+                *reinterpret_cast<uint4*>(p.q_out + ((r0 + r) * p.q_heads + h) * D + d0) = w[r];
         }
     }
 }
 
 template <int D, int P>
-__global__ void __launch_bounds__(Shape<D, P>::THREADS) k_kv_append(Params p) {
+__global__ void __launch_bounds__(Shape<D, P>::THREADS, 1024 / Shape<D, P>::THREADS) k_kv_append(Params p) {
     pdl_launch_dependents();
     pdl_wait();
     if ((int)blockIdx.x < p.kv_blocks)
@@ -392,9 +402,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
     p.interleaved = a.interleaved;
     const int64_t slots = a.T / c.page_size + 2 * (int64_t)s.batch;
     const int64_t kv_blocks = slots * c.kv_heads;
-    // one row per block while the rows are few (latency), four once they fill the device
-    p.q_rows = a.T >= 2048 ? 4 : 1;
-    const int64_t q_blocks = a.q_heads ? (a.T + p.q_rows - 1) / p.q_rows : 0;
+    const int64_t q_blocks = (a.T + Q_ROWS - 1) / Q_ROWS;
     if (kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
     p.kv_blocks = (int)kv_blocks;
     const int64_t blocks = kv_blocks + q_blocks;

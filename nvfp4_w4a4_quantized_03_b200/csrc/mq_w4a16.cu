@@ -1,26 +1,32 @@
 // mq_w4a16.cu -- y = x W^T with x in bf16 and W in NVFP4 (mq_linear_w4a16): the
 // projection of a decode step whose activation stays unquantized.
 //
-// Mathematics: y[m, n] = bf16(alpha * 2^12 * sum_k x[m, k] (2^-12 sigma[n, k/16] q[n, k])).
-// sigma q has at most six significant bits, so (2^-12 sigma q) is exact in
-// bf16; the products of mma.m16n8k16 are exact and summed in binary32; one
-// rounding to bf16 at the end.
+// Mathematics: y[m, n] = bf16(alpha * sum over the K slices of 2^e[m] sum_k (2^-e[m] x[m, k]) (sigma q)[n, k]).
+// sigma q has at most six significant bits and lies in 2^-10 .. 2688: exact in
+// f16.  x goes to f16 under a power of two per token that brings the largest
+// magnitude so far of its K slice to [2^13, 2^14): eight significant bits stay
+// exact down to 2^-28 of that maximum, below it an error of 2^-39 of it is
+// left.  So the f16 products of mma.m16n8k16 are those of the exact operands;
+// sums are binary32, with one rounding to bf16 at the end.
+// (bf16 operands would spare x its conversion, but an E2M1 pair goes to f16 in
+// one instruction and to bf16 in five: measured 21.5 us against the present
+// figure for 5 x 24576 x 4096.)
 //
-// An E2M1 code S EE M placed at bits 15, 8..6 of a bf16 is q 2^-126 (the
-// subnormal 0.5 included); times the bf16 sigma 2^114 it is 2^-12 sigma q.
-//
-// Bound: the weight is read once (0.5625 bytes per element).  A block holds
-// 16 RT rows, its warps split K, each lane reads 16 bytes (32 elements, two
-// scale blocks) of a row at a time, and the order of K inside a fragment is
-// free, so what a lane loads is what it multiplies.  The 16 rows of a tile
-// are four runs of four, 32 rows apart: that is where the stored scales of one
-// 64-byte piece belong, so no scale sector is read twice.
+// Bound: the weight is read once (0.5625 bytes per element).  A block holds 128
+// or 256 rows of W and one slice of K, the blocks of a cluster the slices of
+// the same rows; a block's partial sums are added through distributed shared
+// memory in rank order.  Each lane reads 16 bytes (32 elements, two scale
+// blocks) of a row at a time, four steps ahead, and the order of K inside a
+// fragment is free, so what a lane loads is what it multiplies.  A warp's 16
+// rows are four runs of four, 32 rows apart: that is where the stored scales
+// of one 64-byte piece belong, so no scale sector is read twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "../../include/mq.h"
 #include "mq_debug.cuh"
 #include "mq_internal.h"
+#include "mq_kv.cuh"
 #include "mq_ptx.cuh"
 
 namespace mq {
@@ -29,6 +35,8 @@ namespace w4a16 {
 constexpr int WARPS = 8;
 constexpr int THREADS = WARPS * 32;
 constexpr int STEP = 128;                 // K elements of one warp step
+constexpr int SUB = 512;                  // K elements of x converted at a time: a warp's 16 per lane
+constexpr int STEPS = SUB / STEP;
 
 struct Params {
     const __nv_bfloat16* x;               // [M, K]
@@ -36,18 +44,23 @@ struct Params {
     const uint8_t* w_scales;              // atoms of 128 rows x 4 scales
     const float* alpha;
     __nv_bfloat16* y;                     // [M, N]
-    int M, N, K, katoms;
+    int M, N, K, katoms, slice, split;    // slice: K elements per block, a multiple of SUB
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float hi, float lo) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
@@ -56,47 +69,136 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-// Elements i and i + 4 of a word of eight codes, as bf16 pair q 2^-126.
-template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    const uint32_t top = I == 3 ? w : w << (12 - 4 * I);
-    const uint32_t mag = I < 2 ? w << (6 - 4 * I) : w >> (4 * I - 6);
-    return (top & 0x80008000u) | (mag & 0x01C001C0u);
-}
-// Two E4M3 scales -> each twice in a bf16 pair, times 2^114 (exact).
-__device__ __forceinline__ void scale_pairs(uint16_t s, uint32_t (&f)[2]) {
-    const uint32_t h = cvt_e4m3x2_to_f16x2(s);
-    const __half2 v = *reinterpret_cast<const __half2*>(&h);
-    const float k = __uint_as_float((114u + 127u) << 23);
-    const float lo = __low2float(v) * k, hi = __high2float(v) * k;
-    f[0] = cvt_bf16x2(lo, lo);
-    f[1] = cvt_bf16x2(hi, hi);
+// Eight E2M1 codes -> four f16 pairs (exact), element 0 in the low half of h[0].
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
 template <int NT, int RT>
-__global__ void __launch_bounds__(THREADS) k_linear_w4a16(Params p) {
-    constexpr int ROWS = 16 * RT, MP = 8 * NT;
-    extern __shared__ float part[];                    // [WARPS][MP][ROWS]
+struct Shape {
+    static constexpr int MP = 8 * NT, ROWS = 128 * RT;
+    static constexpr int X_BYTES = 2 * MP * SUB * 2;     // two turns
+    static constexpr int AHEAD = 4 / RT;                 // steps of W in registers
+    static constexpr int TOKENS = MP / WARPS;            // tokens a warp converts
+    static constexpr int PER_SM = NT == 1 ? 3 : 2;       // blocks, by registers
+    static constexpr int PART_BYTES = MP * ROWS * 4;
+    static constexpr int SMEM = X_BYTES > PART_BYTES ? X_BYTES : PART_BYTES;
+};
+
+template <int NT, int RT>
+__global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16(Params p) {
+    using S = Shape<NT, RT>;
+    constexpr int MP = S::MP, ROWS = S::ROWS, AHEAD = S::AHEAD, TOKENS = S::TOKENS;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float s_ratio[2][MP];                   // what a token's sums so far are to be multiplied with
+    __shared__ float s_up[MP];                         // 2^e of each token
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
-    // tile rows: base + (r & 3) + 32 (r >> 2)
-    const int tiles = blockIdx.x * RT;
-    int row[RT][2];
+    const uint32_t rank = cluster_ctarank();
+    const int block = blockIdx.x / p.split;            // rows [block ROWS, ...)
+    const int k_lo = (int)rank * p.slice, k_hi = min(p.K, k_lo + p.slice);
+
+    // W's rows of this block toward L2 before the wait for the previous grid:
+    // a prefetch leaves nothing visible
+    if (tid < ROWS && block * ROWS + tid < p.N && k_hi > k_lo)
+        bulk_prefetch_l2(p.w_codes + (int64_t)(block * ROWS + tid) * (p.K / 2) + k_lo / 2, (k_hi - k_lo) / 2);
+
+    // the warp's tile in each atom of 128 rows: rows 4 warp + (r & 3) + 32 (r >> 2)
     const uint8_t* codes[RT][2];
     const uint8_t* scales[RT][2];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int tile = tiles + i, r = g + 8 * h;
-            const int atom = tile >> 3, in = (tile & 7) * 4 + (r & 3);     // row % 32
-            row[i][h] = atom * 128 + in + 32 * (r >> 2);
-            const int rc = min(row[i][h], p.N - 1);                        // rows behind N: read, not written
-            codes[i][h] = p.w_codes + (int64_t)rc * (p.K / 2) + t * 16;
-            const int atom_c = min(atom, (p.N + 127) / 128 - 1);
-            scales[i][h] = p.w_scales + ((int64_t)atom_c * p.katoms + (t >> 1)) * 512 + in * 16 + (r >> 2) * 4 + 2 * (t & 1);
+            const int r = g + 8 * h, in = warp * 4 + (r & 3);
+            const int atom = min(block * RT + i, (p.N + 127) / 128 - 1);
+            const int row = min(block * ROWS + i * 128 + in + 32 * (r >> 2), p.N - 1);    // behind N: read, not written
+            codes[i][h] = p.w_codes + (int64_t)row * (p.K / 2) + k_lo / 2 + t * 16;
+            scales[i][h] = p.w_scales + ((int64_t)atom * p.katoms + k_lo / 64 + (t >> 1)) * 512 + in * 16 + (r >> 2) * 4 + 2 * (t & 1);
         }
+    // K is a multiple of 64: where the slice ends in half a step, its upper
+    // lanes read what the lower ones do; X is zero there
+    const int steps = (k_hi - k_lo + STEP - 1) / STEP;
+    const int half_step = (k_hi - k_lo) % STEP != 0 && t >= 2 ? steps - 1 : -1;
     pdl_launch_dependents();
     pdl_wait();
+
+    uint4 cw[AHEAD][RT][2];
+    uint16_t sw[AHEAD][RT][2];
+    auto load = [&](int a, int step, int at) {             // `at`: steps from where the pointers stand
+        if (step < steps) {
+            const int ch = step == half_step ? -32 : 0, sh = step == half_step ? -512 : 0;
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    cw[a][i][h] = load_stream(codes[i][h] + ch + at * (STEP / 2));
+                    sw[a][i][h] = *reinterpret_cast<const uint16_t*>(scales[i][h] + sh + at * (STEP / 64 * 512));
+                }
+        }
+    };
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) load(a, a, a);
+
+    // X, 512 columns at a time: a warp converts tokens warp, warp + 8, ..., 16
+    // elements per lane, under the largest exponent of the token so far
+    int e_run[TOKENS];
+    constexpr int BATCH = TOKENS < 4 ? TOKENS : 4;         // tokens held in registers, loaded a turn ahead if that is all
+    uint4 xw[BATCH][2];
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) e_run[i] = -113;
+    auto load_x = [&](int k0, int first) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m = warp + WARPS * (first + i), k = k0 + h * 256 + lane * 8;
+                xw[i][h] = make_uint4(0, 0, 0, 0);
+                if (m < p.M && k < k_hi) xw[i][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K + k));
+            }
+    };
+    auto convert = [&](int turn, int first) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int m = warp + WARPS * (first + i);
+            if (m >= p.M) break;
+            float top = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t u[4] = {xw[i][h].x, xw[i][h].y, xw[i][h].z, xw[i][h].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+            }
+            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            const int e = max(e_run[first + i], (int)(bits >> 23) - 127 - 13);        // the maximum to [2^13, 2^14)
+            if (lane == 0) {
+                s_ratio[turn][m] = exp2i(max(-126, e_run[first + i] - e));
+                s_up[m] = exp2i(e);
+            }
+            e_run[first + i] = e;
+            const float d = exp2i(-e);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 w = xw[i][h];
+                uint4 f;
+                f.x = pack_f16(__uint_as_float(w.x & 0xFFFF0000u) * d, __uint_as_float(w.x << 16) * d);
+                f.y = pack_f16(__uint_as_float(w.y & 0xFFFF0000u) * d, __uint_as_float(w.y << 16) * d);
+                f.z = pack_f16(__uint_as_float(w.z & 0xFFFF0000u) * d, __uint_as_float(w.z << 16) * d);
+                f.w = pack_f16(__uint_as_float(w.w & 0xFFFF0000u) * d, __uint_as_float(w.w << 16) * d);
+                // as the fragments are read: [step][8 elements of a lane's 32][token][lane quarter]
+                const int v = h * 32 + lane;
+                *reinterpret_cast<uint4*>(smem + turn * (MP * SUB * 2) +
+                                          ((((v >> 4) * 4 + (v & 3)) * MP + m) * 4 + ((v >> 2) & 3)) * 16) = f;
+            }
+        }
+    };
+    load_x(k_lo, 0);
 
     float acc[RT][NT][4];
 #pragma unroll
@@ -104,110 +206,147 @@ __global__ void __launch_bounds__(THREADS) k_linear_w4a16(Params p) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
 
-    uint4 cw[RT][2];
-    uint16_t sw[RT][2];
-    auto load = [&](int k0) {
-        // K is a multiple of 64: of the last step the upper lanes may hold nothing
-        const bool in = k0 + 32 * t < p.K;
+    int turn = 0;
+    for (int k0 = k_lo, step0 = 0; k0 < k_hi; k0 += SUB, step0 += STEPS, turn ^= 1) {
+        // Two turns of shared memory and one barrier: whoever writes a turn has
+        // passed the barrier behind which the other one was read last.
+        convert(turn, 0);
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                cw[i][h] = make_uint4(0, 0, 0, 0);
-                sw[i][h] = 0;
-                if (in) {
-                    cw[i][h] = load_stream(codes[i][h] + k0 / 2);
-                    sw[i][h] = *reinterpret_cast<const uint16_t*>(scales[i][h] + (int64_t)(k0 / 64) * 512);
-                }
-            }
-    };
-    int k0 = warp * STEP;
-    if (k0 < p.K) load(k0);
-    for (; k0 < p.K; k0 += WARPS * STEP) {
-        uint4 c[RT][2];
-        uint32_t sf[RT][2][2];
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                c[i][h] = cw[i][h];
-                scale_pairs(sw[i][h], sf[i][h]);
-            }
-        if (k0 + WARPS * STEP < p.K) load(k0 + WARPS * STEP);
-        const bool in = k0 + 32 * t < p.K;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {                  // words of eight codes; scale block j / 2 of the lane's two
-            uint32_t b[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                uint4 xv = make_uint4(0, 0, 0, 0);
-                if (in && n * 8 + g < p.M)
-                    xv = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(n * 8 + g) * p.K + k0 + 32 * t + 8 * j));
-                b[n][0] = __byte_perm(xv.x, xv.z, 0x5410);     // elements 0, 4
-                b[n][1] = __byte_perm(xv.x, xv.z, 0x7632);     // 1, 5
-                b[n][2] = __byte_perm(xv.y, xv.w, 0x5410);     // 2, 6
-                b[n][3] = __byte_perm(xv.y, xv.w, 0x7632);     // 3, 7
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const uint32_t w0 = j == 0 ? c[i][0].x : j == 1 ? c[i][0].y : j == 2 ? c[i][0].z : c[i][0].w;
-                const uint32_t w1 = j == 0 ? c[i][1].x : j == 1 ? c[i][1].y : j == 2 ? c[i][1].z : c[i][1].w;
-                const uint32_t s0 = sf[i][0][j >> 1], s1 = sf[i][1][j >> 1];
-                const uint32_t a0[4] = {mul_bf16x2(code_pair<0>(w0), s0), mul_bf16x2(code_pair<0>(w1), s1),
-                                        mul_bf16x2(code_pair<1>(w0), s0), mul_bf16x2(code_pair<1>(w1), s1)};
-                const uint32_t a1[4] = {mul_bf16x2(code_pair<2>(w0), s0), mul_bf16x2(code_pair<2>(w1), s1),
-                                        mul_bf16x2(code_pair<3>(w0), s0), mul_bf16x2(code_pair<3>(w1), s1)};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_bf16(acc[i][n], a0, b[n][0], b[n][1]);
-                    mma_bf16(acc[i][n], a1, b[n][2], b[n][3]);
-                }
-            }
+        for (int first = BATCH; first < TOKENS; first += BATCH) {
+            load_x(k0, first);
+            convert(turn, first);
         }
+        if (k0 + SUB < k_hi) load_x(k0 + SUB, 0);
+        __syncthreads();
+        if (k0 > k_lo) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float r = s_ratio[turn][n * 8 + 2 * t + e];
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        acc[i][n][e] *= r;
+                        acc[i][n][e + 2] *= r;
+                    }
+                }
+        }
+        const uint8_t* xs = smem + turn * (MP * SUB * 2);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (step0 + s >= steps) break;
+            const int a = s % AHEAD;
+            uint32_t sf[RT][2][2];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t v = cvt_e4m3x2_to_f16x2(sw[a][i][h]);
+                    sf[i][h][0] = __byte_perm(v, v, 0x1010);
+                    sf[i][h][1] = __byte_perm(v, v, 0x3232);
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {              // words of eight codes; scale block j / 2 of the lane's two
+                uint4 b[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    b[n] = *reinterpret_cast<const uint4*>(xs + (((s * 4 + j) * MP + n * 8 + g) * 4 + t) * 16);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const uint4 &c0 = cw[a][i][0], &c1 = cw[a][i][1];
+                    const uint32_t w0 = j == 0 ? c0.x : j == 1 ? c0.y : j == 2 ? c0.z : c0.w;
+                    const uint32_t w1 = j == 0 ? c1.x : j == 1 ? c1.y : j == 2 ? c1.z : c1.w;
+                    uint32_t h0[4], h1[4];
+                    decode8(w0, h0);
+                    decode8(w1, h1);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        h0[q] = mul_f16x2(h0[q], sf[i][0][j >> 1]);
+                        h1[q] = mul_f16x2(h1[q], sf[i][1][j >> 1]);
+                    }
+                    const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(acc[i][n], a0, b[n].x, b[n].y);
+                        mma_f16(acc[i][n], a1, b[n].z, b[n].w);
+                    }
+                }
+            }
+            load(a, step0 + s + AHEAD, s + AHEAD);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                codes[i][h] += SUB / 2;
+                scales[i][h] += SUB / 64 * 512;
+            }
     }
-    // acc: rows g (0, 1) and g + 8 (2, 3) of a tile, tokens 2t and 2t + 1
+    // acc: rows g (0, 1) and g + 8 (2, 3) of a tile, tokens 2t and 2t + 1, to [token][row of the block]
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                part[(warp * MP + n * 8 + 2 * t + (e & 1)) * ROWS + i * 16 + g + 8 * (e >> 1)] = acc[i][n][e];
-    __syncthreads();
-    const float scale = __fmul_rn(__ldg(p.alpha), 4096.f);
-    for (int i = tid; i < p.M * ROWS; i += THREADS) {
-        const int m = i / ROWS, r = i % ROWS;
-        float sum = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const int m = n * 8 + 2 * t + (e & 1), r = g + 8 * (e >> 1);
+                if (m < p.M)
+                    part[m * ROWS + i * 128 + warp * 4 + (r & 3) + 32 * (r >> 2)] = k_hi > k_lo ? acc[i][n][e] * s_up[m] : 0.f;
+            }
+    if (p.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    // the cluster's blocks finish a share of the outputs each, partial sums added in rank order
+    const float alpha = __ldg(p.alpha);
+    const float* peer[8];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) sum += part[(w * MP + m) * ROWS + r];
-        const int tile = tiles + r / 16, rr = r % 16;
-        const int n = (tile >> 3) * 128 + (tile & 7) * 4 + (rr & 3) + 32 * (rr >> 2);
+    for (int q = 0; q < 8; ++q) peer[q] = q < p.split ? map_shared_rank(part, (uint32_t)q) : part;
+    for (int i = (int)rank * THREADS + tid; i < p.M * ROWS; i += p.split * THREADS) {
+        float sum = peer[0][i];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+            if (q < p.split) sum += peer[q][i];
+        const int m = i / ROWS, n = block * ROWS + i % ROWS;
         if (n < p.N && MQ_CHECK((int64_t)m * p.N + n < (int64_t)p.M * p.N))
-            p.y[(int64_t)m * p.N + n] = __float2bfloat16_rn(sum * scale);
+            p.y[(int64_t)m * p.N + n] = __float2bfloat16_rn(sum * alpha);
     }
+    if (p.split > 1) cluster_sync();                   // peers' shared memory is read until here
 }
 
 MQ_DEBUG_READER(debug_hits_w4a16)
 
 template <int NT, int RT>
-cudaError_t launch(const Params& p, cudaStream_t stream) {
-    constexpr int SMEM = WARPS * 8 * NT * 16 * RT * 4;
+cudaError_t launch(Params p, int num_sms, cudaStream_t stream) {
+    using S = Shape<NT, RT>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     const int d = dev < 64 ? dev : 63;
     if (!attr_set[d]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_w4a16<NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        cudaError_t e = cudaFuncSetAttribute(k_linear_w4a16<NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
         attr_set[d] = true;
     }
+    const int blocks = (p.N + S::ROWS - 1) / S::ROWS;
+    // split K (a power of two, at most 8) while a block keeps 512 columns and
+    // all blocks run at once (a second wave of few blocks costs as much as the first)
+    int split = 1;
+    while (split < 8 && (int64_t)blocks * split * 2 <= S::PER_SM * (int64_t)num_sms && (p.K + SUB - 1) / SUB >= 2 * split) split *= 2;
+    p.split = split;
+    p.slice = ((p.K + SUB - 1) / SUB + split - 1) / split * SUB;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    int nattr = 0;
-    const int tiles = (p.N + 127) / 128 * 8;
-    cfg.gridDim = dim3((tiles + RT - 1) / RT);
+    cudaLaunchAttribute attr[2];
+    int nattr = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(blocks * split);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = stream;
     set_pdl_attr(attr, &nattr);
     cfg.attrs = attr;
@@ -221,13 +360,12 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
 cudaError_t launch_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8_t* w_codes, const uint8_t* w_scales,
                                 const float* alpha_w, int64_t N, void* y, int num_sms, cudaStream_t stream) {
     using namespace w4a16;
-    (void)num_sms;
     Params p{static_cast<const __nv_bfloat16*>(x), w_codes, w_scales, alpha_w, static_cast<__nv_bfloat16*>(y),
-             (int)M, (int)N, (int)K, (int)scale_atom_cols(K)};
-    if (M <= 8) return launch<1, 1>(p, stream);
-    if (M <= 16) return launch<2, 1>(p, stream);
-    if (M <= 32) return launch<4, 2>(p, stream);
-    return launch<8, 2>(p, stream);
+             (int)M, (int)N, (int)K, (int)scale_atom_cols(K), 0, 1};
+    if (M <= 8) return launch<1, 1>(p, num_sms, stream);
+    if (M <= 16) return launch<2, 1>(p, num_sms, stream);
+    if (M <= 32) return launch<4, 1>(p, num_sms, stream);
+    return launch<8, 1>(p, num_sms, stream);
 }
 
 }  // namespace mq
