@@ -54,34 +54,56 @@ __device__ __forceinline__ void kv_write_out(const KvAttendParams& p, int c0, in
             make_uint2(cvt_bf16x2(acc.y * inv, acc.x * inv), cvt_bf16x2(acc.w * inv, acc.z * inv));
 }
 
-// Joins a cell's chunks in their order: part is [chunk][rows_cap][D values, M, l].
+// A cell's partial results: [chunk][row][D] values, then [chunk][row] pairs (M, l),
+// for p.chunks chunks of rows_cap rows.
 template <int D>
-__device__ __forceinline__ void kv_join(const KvAttendParams& p, const float* part, int chunks, int rows_cap,
-                                        int nrows, int c0, int64_t row0, int head, int tid, int threads) {
+__device__ __forceinline__ float* kv_part_ml(const KvAttendParams& p, float* part, int rows_cap) {
+    return part + (int64_t)p.chunks * rows_cap * D;
+}
+
+// Joins the first `chunks` of them in their order; `weights`: shared memory of nrows * chunks floats.
+template <int D>
+__device__ __forceinline__ void kv_join(const KvAttendParams& p, float* part, int chunks, int rows_cap,
+                                        int nrows, int c0, int64_t row0, int head, int tid, int threads,
+                                        float* weights) {
     constexpr int V4 = D / 4;
-    const int64_t step = (int64_t)rows_cap * (D + 2);
+    const int64_t step = (int64_t)rows_cap * D;
+    const float2* ml = reinterpret_cast<const float2*>(kv_part_ml<D>(p, part, rows_cap));
+    const int lane = tid % 32;
+    // each row's maximum and the chunks' weights 2^(M - max) / sum: a warp per row
+    for (int r = tid / 32; r < nrows; r += threads / 32) {
+        float top = -INFINITY;
+        for (int c = lane; c < chunks; c += 32) top = fmaxf(top, __ldcg(&ml[c * rows_cap + r].x));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float lsum = 0.f;
+        for (int c = lane; c < chunks; c += 32) {
+            const float2 v = __ldcg(&ml[c * rows_cap + r]);
+            const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
+            weights[r * chunks + c] = f;
+            lsum = __fmaf_rn(v.y, f, lsum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+        // a row that saw nothing: zero
+        const float inv = lsum > 0.f || lsum != lsum ? __fdiv_rn(1.f, lsum) : 0.f;
+        for (int c = lane; c < chunks; c += 32) weights[r * chunks + c] *= inv;
+    }
+    __syncthreads();
     for (int i = tid; i < nrows * V4; i += threads) {
         const int r = i / V4, c4 = i % V4;
-        const float* src = part + (int64_t)r * (D + 2);
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int c = 0; c < chunks; ++c) top = fmaxf(top, __ldcg(src + c * step + D));
+        const float4* src = reinterpret_cast<const float4*>(part + (int64_t)r * D + c4 * 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
-#pragma unroll 4
+#pragma unroll 16
         for (int c = 0; c < chunks; ++c) {
-            const float* pc = src + c * step;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + D));
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4));
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(pc + c4 * 4 + 2));
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+            const float4 x = __ldcg(src + c * (step / 4));
+            const float f = weights[r * chunks + c];
             acc.x = __fmaf_rn(x.x, f, acc.x);
             acc.y = __fmaf_rn(x.y, f, acc.y);
-            acc.z = __fmaf_rn(y.x, f, acc.z);
-            acc.w = __fmaf_rn(y.y, f, acc.w);
-            lsum = __fmaf_rn(ml.y, f, lsum);
+            acc.z = __fmaf_rn(x.z, f, acc.z);
+            acc.w = __fmaf_rn(x.w, f, acc.w);
         }
-        kv_write_out<D>(p, c0, row0 + r, head, c4, acc, lsum);
+        kv_write_out<D>(p, c0, row0 + r, head, c4, acc, 1.f);
     }
 }
 

@@ -25,7 +25,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <algorithm>
 
 #include "../../include/mq.h"
 #include "mq_debug.cuh"
@@ -40,7 +39,6 @@ namespace kv_attend {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int STEP = 16;                 // tokens of one warp step
-constexpr int SEGMENT = 4096;            // tokens whose pages are held at a time
 constexpr float LAZY = 8.f;              // M moves when a weight would pass 2^LAZY
 constexpr float BIAS = 6.f;              // weights are held times 2^BIAS: 2^14 at most, f16 holds 2^16
 
@@ -73,21 +71,13 @@ __device__ __forceinline__ void load_codes(uint32_t (&w)[N], const uint8_t* p) {
     }
 }
 
-// What a lane keeps of the pages of its chunk.
-struct PageInfo {
-    int64_t base;      // byte offset of (page, head) in either cache, -1: not to be read
-    float ck, ev, iev; // 2^ek, ev, 2^-ev
-    float pad;
-};
-
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) k_kv_attend(Params p) {
     constexpr int ROWS = 8 * NT;
     constexpr int KH = D / 64;               // 16-byte pieces of a K row per lane
     constexpr int VW = D / 32;               // words of a V row per lane
     constexpr int MT = D / 16;               // 16-wide slices of d
-    extern __shared__ uint8_t smem[];
-    PageInfo* pages = reinterpret_cast<PageInfo*>(smem);
+    extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait();
@@ -108,20 +98,27 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
         if (tid == 0 && p.status) atomicExch(p.status, MQ_ERR_INVALID_ARG);
         return;
     }
+    // positions and rows stay below 2^31 - 2^16 (checked by the entry point)
     const int rows = n * p.group, row0 = tile * ROWS;
     if (row0 >= rows) return;
-    const int64_t start = len - n;                              // position of the first new token
+    const int start = (int)len - n;                             // position of the first new token
     const int last_row = min(rows, row0 + ROWS) - 1;
-    const int64_t end = max((int64_t)0, min(len, start + last_row / p.group + 1));   // keys that some row sees
-    const int chunks = max(1, (int)((end + p.chunk_tokens - 1) / p.chunk_tokens));
+    const int end = max(0, min((int)len, start + last_row / p.group + 1));   // keys that some row sees
+    const int chunks = max(1, (int)(((int64_t)end + p.chunk_tokens - 1) / p.chunk_tokens));
     if (chunk >= chunks) return;
-    const int64_t k0 = (int64_t)chunk * p.chunk_tokens, k1 = min(end, k0 + p.chunk_tokens);
-    const int64_t sees_all = start + row0 / p.group;            // keys up to this position: every row sees them
+    const int k0 = chunk * p.chunk_tokens, k1 = (int)min((int64_t)end, (int64_t)k0 + p.chunk_tokens);
+    const int sees_all = start + row0 / p.group;                // keys up to this position: every row sees them
+
+    // The warp's steps of 16 keys: the page of the step after the next is
+    // looked up while the codes and scales of the next are on their way.
+    const int* table = p.table + (int64_t)b * p.max_pages;
+    auto page_of = [&](int tok0) { return tok0 < k1 ? __ldg(table + (tok0 >> p.page_log2)) : -1; };
+    int page = page_of(k0 + warp * STEP);
 
     // Q: row g of each n-tile, the d that the K fragments hold: 16 t .. 16 t + 15 (+ 64)
     uint32_t qf[NT][4 * KH][2];
     float fac[NT][2];                        // scale * log2(e) * 2^(row's exponent) of rows 2t, 2t + 1
-    int64_t pos[NT][2];                      // their positions (-1: no row)
+    int pos[NT][2];                          // their positions (-1: no row)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + g;
@@ -177,71 +174,54 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
             for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
     }
 
-    // segment by segment: its pages, then its keys, 16 tokens per warp at a time
-    for (int64_t s0 = k0; s0 < k1; s0 += SEGMENT) {
-    const int64_t s1 = min(k1, s0 + SEGMENT);
-    const int64_t page0 = s0 >> p.page_log2;
-    const int npages = (int)(((s1 - 1) >> p.page_log2) - page0 + 1);
-    __syncthreads();
-    for (int i = tid; i < npages; i += THREADS) {
-        PageInfo info{-1, 0.f, 0.f, 0.f, 0.f};
-        const int64_t page = p.table[(int64_t)b * p.max_pages + page0 + i];
-        if (page >= 0 && page < p.num_pages) {
-            const int64_t cell = page * p.kv_heads + head;
-            const float sk = p.k_scales[cell], sv = p.v_scales[cell];
-            info.base = cell * ((int64_t)page_tokens * D);
-            info.ck = sk;
-            info.ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);
-            info.iev = __uint_as_float((254u << 23) - (__float_as_uint(sv) & 0x7F800000u));
-        } else if (p.status) {
-            atomicExch(p.status, MQ_ERR_INVALID_ARG);
-        }
-        pages[i] = info;
-    }
-    __syncthreads();
-
     uint32_t kw[2][KH][4], vw[4][VW];
-    auto load_k = [&](int64_t tok0) {
-        const PageInfo& pg = pages[(tok0 >> p.page_log2) - page0];
-        const int64_t off = pg.base + (int64_t)(tok0 & (page_tokens - 1)) * D;
+    float sk = 0.f, sv = 1.f;                // the pages' scales of the step whose codes are on their way
+    bool valid = false;
+    int64_t base = 0;                        // byte offset of its first code
+    [[maybe_unused]] const int64_t pool = (p.num_pages * p.kv_heads << p.page_log2) * D;
+    auto load_k = [&](int tok0) {
+        valid = page >= 0 && page < p.num_pages;
+        if (!valid && p.status && lane == 0) atomicExch(p.status, MQ_ERR_INVALID_ARG);
+        const int64_t cell = valid ? (int64_t)page * p.kv_heads + head : 0;
+        base = ((cell << p.page_log2) + (tok0 & (page_tokens - 1))) * D;
+        sk = __ldg(p.k_scales + cell);
+        sv = __ldg(p.v_scales + cell);
+        const uint8_t* src = p.k_codes + base + g * D + t * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < KH; ++h) {
-                if (pg.base >= 0 && MQ_CHECK(off + (g + 8 * i) * D + h * 64 + t * 16 + 16 <=
-                                             p.num_pages * p.kv_heads * (int64_t)page_tokens * D)) {
-                    load_codes(kw[i][h], p.k_codes + off + (g + 8 * i) * D + h * 64 + t * 16);
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) kw[i][h][w] = 0;
-                }
+                if (MQ_CHECK(base + (g + 8 * i) * D + h * 64 + t * 16 + 16 <= pool)) load_codes(kw[i][h], src + i * 8 * D + h * 64);
             }
+        page = page_of(tok0 + WARPS * STEP);
     };
-    auto load_v = [&](int64_t tok0) {
-        const PageInfo& pg = pages[(tok0 >> p.page_log2) - page0];
-        const int64_t off = pg.base + (int64_t)(tok0 & (page_tokens - 1)) * D;
+    auto load_v = [&](int tok0) {
+        const uint8_t* src = p.v_codes + base + 2 * t * D + g * (VW * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
+        for (int i = 0; i < 4; ++i)
+            if (MQ_CHECK(base + (2 * t + (i & 1) + 8 * (i >> 1)) * D + (g + 1) * (VW * 4) <= pool))
+                load_codes(vw[i], src + ((i & 1) + 8 * (i >> 1)) * D);
+        if (tok0 + STEP > k1) {
             // behind the last token a page holds whatever was there: a NaN code times a zero weight is no zero
-            if (pg.base >= 0 && tok0 + tok < s1 && MQ_CHECK(off + tok * D + (g + 1) * (VW * 4) <=
-                                                            p.num_pages * p.kv_heads * (int64_t)page_tokens * D)) {
-                load_codes(vw[i], p.v_codes + off + tok * D + g * (VW * 4));
-            } else {
 #pragma unroll
-                for (int w = 0; w < VW; ++w) vw[i][w] = 0;
-            }
+            for (int i = 0; i < 4; ++i)
+                if (tok0 + 2 * t + (i & 1) + 8 * (i >> 1) >= k1) {
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) vw[i][w] = 0;
+                }
         }
     };
 
-    int64_t tok0 = s0 + warp * STEP;
-    if (tok0 < s1) {
+    int tok0 = k0 + warp * STEP;
+    if (tok0 < k1) {
         load_k(tok0);
         load_v(tok0);
     }
-    for (; tok0 < s1; tok0 += WARPS * STEP) {
-        const PageInfo pg = pages[(tok0 >> p.page_log2) - page0];
-        const int64_t next = tok0 + WARPS * STEP;
+    for (; tok0 < k1; tok0 += WARPS * STEP) {
+        const int next = tok0 + WARPS * STEP;
+        const float ck = sk, ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);
+        const float iev = __uint_as_float((254u << 23) - (__float_as_uint(sv) & 0x7F800000u));
+        const bool here = valid;
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -255,19 +235,19 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a, qf[nt][4 * h + st][0], qf[nt][4 * h + st][1]);
             }
-        if (next < s1) load_k(next);
+        if (next < k1) load_k(next);
 
         // s[nt]: tokens g (0, 1) and g + 8 (2, 3), rows 2t and 2t + 1
-        const bool masked = tok0 + STEP - 1 > sees_all || pg.base < 0;
+        const bool masked = tok0 + STEP - 1 > sees_all || !here;
         bool higher = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float u = __fmaf_rn(s[nt][i], fac[nt][i & 1] * pg.ck, pg.ev);
+                float u = __fmaf_rn(s[nt][i], fac[nt][i & 1] * ck, ev);
                 if (masked) {
-                    const int64_t at = tok0 + g + 8 * (i >> 1);
-                    u = at <= pos[nt][i & 1] && at < s1 && pg.base >= 0 ? u : -INFINITY;
+                    const int at = tok0 + g + 8 * (i >> 1);
+                    u = at <= pos[nt][i & 1] && at < k1 && here ? u : -INFINITY;
                 }
                 s[nt][i] = u;
                 higher |= u > m[nt][i & 1] + LAZY;
@@ -301,7 +281,7 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
             for (int i = 0; i < 4; ++i) {
                 const float mm = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
                 w[i] = ex2(s[nt][i] - mm + BIAS);
-                l[nt][i & 1] = __fmaf_rn(w[i], pg.iev, l[nt][i & 1]);
+                l[nt][i & 1] = __fmaf_rn(w[i], iev, l[nt][i & 1]);
             }
             pf[nt][0] = movmatrix(pack_f16(w[1], w[0]));
             pf[nt][1] = movmatrix(pack_f16(w[3], w[2]));
@@ -317,12 +297,10 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][j], a, pf[nt][0], pf[nt][1]);
         }
-        if (next < s1) load_v(next);
-    }
+        if (next < k1) load_v(next);
     }
 
     // ---- merge the warps: lane (g, t) holds rows 8 nt + 2 t and + 1, d = g D/8 ...
-    __syncthreads();                                           // the page list is done with
     float* mm = reinterpret_cast<float*>(smem);                // [WARPS][ROWS]
     float* ll = mm + WARPS * ROWS;                             // [WARPS][ROWS]
     float* oo = ll + WARPS * ROWS;                             // [WARPS][ROWS][D]
@@ -346,7 +324,7 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
     __syncthreads();
     constexpr int V4 = D / 4;
     const int64_t cell = ((int64_t)b * p.row_tiles + tile) * p.kv_heads + head;
-    float* part_ml = p.part ? p.part + cell * p.chunks * (int64_t)(ROWS * (D + 2)) : nullptr;
+    float* part = p.part ? p.part + cell * p.chunks * (int64_t)(ROWS * (D + 2)) : nullptr;
     const int nrows = last_row - row0 + 1;
     for (int i = tid; i < nrows * V4; i += THREADS) {
         const int r = i / V4, c4 = i % V4;
@@ -369,11 +347,9 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
         if (chunks == 1) {
             kv_write_out<D>(p, c0, row0 + r, head, c4, acc, lsum);
         } else {
-            // [chunk][row]: D values, M, l
-            float* dst = part_ml + ((int64_t)chunk * ROWS + r) * (D + 2);
-            *reinterpret_cast<float2*>(dst + c4 * 4) = make_float2(acc.x, acc.y);
-            *reinterpret_cast<float2*>(dst + c4 * 4 + 2) = make_float2(acc.z, acc.w);
-            if (c4 == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, lsum);
+            *reinterpret_cast<float4*>(part + ((int64_t)chunk * ROWS + r) * D + c4 * 4) = acc;
+            if (c4 == 0)
+                reinterpret_cast<float2*>(kv_part_ml<D>(p, part, ROWS))[chunk * ROWS + r] = make_float2(top, lsum);
         }
     }
     if (chunks == 1) return;
@@ -389,21 +365,20 @@ __global__ void __launch_bounds__(THREADS) k_kv_attend(Params p) {
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    kv_join<D>(p, part_ml, chunks, ROWS, nrows, c0, row0, head, tid, THREADS);
+    kv_join<D>(p, part, chunks, ROWS, nrows, c0, row0, head, tid, THREADS, reinterpret_cast<float*>(smem));
 }
 
 MQ_DEBUG_READER(debug_hits_kv_attend)
 
 template <int D, int NT>
 cudaError_t launch(const Params& p, int64_t blocks, cudaStream_t stream) {
-    constexpr int MERGE = WARPS * 8 * NT * (D + 2) * 4;
-    const int smem = std::max<int>(MERGE, (std::min(p.chunk_tokens, SEGMENT) >> p.page_log2) * sizeof(PageInfo) + sizeof(PageInfo));
+    constexpr int SMEM = WARPS * 8 * NT * (D + 2) * 4;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     const int d = dev < 64 ? dev : 63;
     if (!attr_set[d]) {
-        cudaError_t e = cudaFuncSetAttribute(k_kv_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 << 10);
+        cudaError_t e = cudaFuncSetAttribute(k_kv_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         attr_set[d] = true;
     }
@@ -412,7 +387,7 @@ cudaError_t launch(const Params& p, int64_t blocks, cudaStream_t stream) {
     int nattr = 0;
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     set_pdl_attr(attr, &nattr);
     cfg.attrs = attr;

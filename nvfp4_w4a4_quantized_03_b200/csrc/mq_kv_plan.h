@@ -22,7 +22,7 @@ struct KvPlan {
 
 inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
                       int64_t max_len) {
-    constexpr int64_t TICKETS = 148 * 10;
+    constexpr int64_t TICKETS = 592;
     KvPlan p{};
     const int64_t rows = max_q * (q_heads / kv_heads);
     p.prefill = rows > 16;
@@ -31,14 +31,15 @@ inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t 
     p.row_tiles = (rows + p.block_rows - 1) / p.block_rows;
     p.cells = batch * p.row_tiles * kv_heads;
     // one chunk where the cells fill the device (one block of the tcgen05 form
-    // per SM; two waves of five blocks of the other); else enough chunks to do
-    // so, at most 64 (the last block to finish a cell reads them all) unless
-    // that makes them shorter than 1024 tokens
-    const int64_t fill = p.prefill ? 148 : TICKETS;
-    int64_t c = std::max<int64_t>(max_len, 64);
-    if (p.cells < fill)
-        c = std::max<int64_t>(p.prefill ? 256 : 64, std::min(std::max<int64_t>(1024, (max_len + 63) / 64),
-                                                            (p.cells * max_len + fill - 1) / fill));
+    // per SM; four of the other); else enough chunks to do
+    // so, of 128 (256) tokens at least and of 1024 at most, but never more than
+    // 128 (64) of them: the last block to finish a cell reads them all
+    const int64_t fill = p.prefill ? 148 : 592;
+    int64_t c = std::max<int64_t>(max_len, 128);
+    if (p.cells < fill) {
+        const int64_t want = (p.cells * max_len + fill - 1) / fill, most = p.prefill ? 64 : 128;
+        c = std::max({std::min<int64_t>(want, 1024), (max_len + most - 1) / most, (int64_t)(p.prefill ? 256 : 128)});
+    }
     p.chunk_tokens = (c + 127) / 128 * 128;
     if (!p.prefill) p.chunk_tokens = (c + 63) / 64 * 64;
     p.chunks = std::max<int64_t>(1, (max_len + p.chunk_tokens - 1) / p.chunk_tokens);

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         tc_fence_after();
         const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;       // a row that sees nothing: zero
         const int64_t at = ((int64_t)(c0 + row / p.group) * p.q_heads + head * p.group + row % p.group) * D;
-        float* dst = part ? part + ((int64_t)chunk * ROWS + tid) * (D + 2) : nullptr;
+        float* dst = part ? part + ((int64_t)chunk * ROWS + tid) * D : nullptr;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t v[32];
@@ -629,13 +629,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        *reinterpret_cast<float2*>(dst + c + i) =
-                            make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
         }
-        if (chunks > 1 && row < rows) *reinterpret_cast<float2*>(dst + D) = make_float2(m, l);
+        if (chunks > 1 && row < rows)
+            reinterpret_cast<float2*>(kv_part_ml<D>(p, part, ROWS))[chunk * ROWS + tid] = make_float2(m, l);
         tc_fence_before();
     }
     __threadfence();
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     __syncthreads();
     if (!s->last) return;
     __threadfence();
-    kv_join<D>(p, part, chunks, ROWS, last_row - row0 + 1, c0, row0, head, tid, THREADS);
+    kv_join<D>(p, part, chunks, ROWS, last_row - row0 + 1, c0, row0, head, tid, THREADS, reinterpret_cast<float*>(base));
 }
 
 MQ_DEBUG_READER(debug_hits_kv_prefill)
