@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     // K is a multiple of 64: where the slice ends in half a step, its upper
     // lanes read what the lower ones do; X is zero there
     const int steps = (k_hi - k_lo + STEP - 1) / STEP;
-    const int half_step = (k_hi - k_lo) % STEP != 0 && t >= 2 ? steps - 1 : -1;
+    const bool half_end = (k_hi - k_lo) % STEP != 0;
     pdl_launch_dependents();
     pdl_wait();
 
@@ -132,13 +132,17 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     uint16_t sw[AHEAD][RT][2];
     auto load = [&](int a, int step, int at) {             // `at`: steps from where the pointers stand
         if (step < steps) {
-            const int ch = step == half_step ? -32 : 0, sh = step == half_step ? -512 : 0;
+            int ch = at * (STEP / 2), sh = at * (STEP / 64 * 512);
+            if (half_end && step == steps - 1 && t >= 2) {
+                ch -= 32;
+                sh -= 512;
+            }
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    cw[a][i][h] = load_stream(codes[i][h] + ch + at * (STEP / 2));
-                    sw[a][i][h] = *reinterpret_cast<const uint16_t*>(scales[i][h] + sh + at * (STEP / 64 * 512));
+                    cw[a][i][h] = load_stream(codes[i][h] + ch);
+                    sw[a][i][h] = *reinterpret_cast<const uint16_t*>(scales[i][h] + sh);
                 }
         }
     };

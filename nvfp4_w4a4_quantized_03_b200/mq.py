@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -24,11 +23,6 @@ MQ_OK = 0
 MQ_ERR_TIMEOUT = -7
 
 _lib = None
-
-
-# mq_kv_cache and mq_kv_batch of mq.h as the bytes the calls read
-_KV_CACHE = struct.Struct("@PPPPqiiii")
-_KV_BATCH = struct.Struct("@PPPqii")
 
 
 class MQError(RuntimeError):
@@ -237,93 +231,32 @@ def mq_mlp_w4a4(x: torch.Tensor, wgu_codes, wgu_scales, alpha_gu, inter: int, wd
                              ws.numel() * ws.element_size(), _stream(stream)), "mq_mlp_w4a4")
 
 
-# The calls of a decode step are short, so their marshalling is too: one pass
-# of checks per tensor, addresses as plain integers, structures packed as bytes.
+# The kernels of a decode step run for a few microseconds, so the checks and the
+# marshalling of its calls are native (csrc/mq_torch.cpp); arguments that it
+# refuses raise ValueError before the library sees them.
 
-_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
-
-
-def _addr(t: torch.Tensor, dtype, dev: int, what: str) -> int:
-    """Address of a contiguous tensor of `dtype` on CUDA device `dev`."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: on {t.device}, expected on cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous tensor expected")
-    return t.data_ptr()
+_calls = None
 
 
-def _current(t: torch.Tensor, what: str) -> int:
-    """The current device, which has to be the tensor's (the library enqueues there)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: device tensor expected")
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{dev}")
-    return dev
-
-
-def _stream_ptr(stream, dev: int) -> int:
-    if stream is None:
-        return _raw_stream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _raw_stream(dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-# the same without a Stream object, where this torch offers it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-
-
-def _row_stride(what: str, t: torch.Tensor, width: int) -> int:
-    """Elements between rows of a bf16 tensor [rows, ...] whose rows hold
-    `width` consecutive elements (rows may be apart)."""
-    if t.dtype is not _BF16:
-        raise ValueError(f"{what}: bfloat16 expected, got {t.dtype}")
-    if t.is_contiguous():
-        return width
-    if not t[0].is_contiguous():
-        raise ValueError(f"{what}: consecutive elements within a row expected")
-    return t.stride(0) if t.shape[0] > 1 else width
+def _load_calls():
+    global _calls
+    if _calls is None:
+        path = os.path.join(_HERE, "_mq_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m nvfp4_w4a4_quantized_03_b200.build`")
+        from . import _mq_torch
+        L = lib()
+        _mq_torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                         for f in (L.mq_linear_w4a16, L.mq_rope_kv_append, L.mq_kv_attention)))
+        _calls = _mq_torch
+    return _calls
 
 
 def mq_linear_w4a16(x: torch.Tensor, w_codes, w_scales, alpha_w, N: int, y: torch.Tensor, stream=None) -> None:
     """y = x W^T, x bf16 [M, K] with M <= 64, W quantized."""
-    dev = _current(x, "x")
-    M, K = x.shape
-    if w_codes.numel() < N * K // 2 or w_scales.numel() < (N + 127) // 128 * 128 * ((K + 63) // 64 * 4):
-        raise ValueError("w_codes, w_scales: smaller than an [N, K] weight's")
-    if y.numel() < M * N:
-        raise ValueError("y: smaller than [M, N]")
-    status = (_lib or lib()).mq_linear_w4a16(
-        _addr(x, _BF16, dev, "x"), M, K, _addr(w_codes, _U8, dev, "w_codes"), _addr(w_scales, _U8, dev, "w_scales"),
-        _addr(alpha_w, _F32, dev, "alpha_w"), N, _addr(y, _BF16, dev, "y"), _stream_ptr(stream, dev))
+    status = (_calls or _load_calls()).linear(x, w_codes, w_scales, alpha_w, N, y, stream)
     if status:
         raise MQError(status, "mq_linear_w4a16")
-
-
-def _kv_args(dev: int, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales):
-    """(mq_kv_cache, mq_kv_batch, kv heads, head_dim, batch) of a call's tensors."""
-    shape = k_codes.shape
-    pages, heads, page, dim = shape
-    codes = k_codes.dtype
-    if codes is not _E4M3 and codes is not _U8:
-        raise ValueError(f"k_codes: float8_e4m3fn or uint8 expected, got {codes}")
-    if v_codes.shape != shape:
-        raise ValueError("v_codes: another shape than k_codes")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
-        raise ValueError("k_scales, v_scales: [pages, kv heads] expected")
-    batch, max_pages = page_table.shape
-    if cu_rows.numel() != batch + 1 or lens.numel() != batch:
-        raise ValueError("cu_rows [batch + 1], lens [batch] and page_table [batch, max_pages] do not agree")
-    return (_KV_CACHE.pack(_addr(k_codes, codes, dev, "k_codes"), _addr(v_codes, codes, dev, "v_codes"),
-                           _addr(k_scales, _F32, dev, "k_scales"), _addr(v_scales, _F32, dev, "v_scales"),
-                           pages, page, heads, dim, 0),
-            _KV_BATCH.pack(_addr(cu_rows, _I32, dev, "cu_rows"), _addr(lens, _I32, dev, "lens"),
-                           _addr(page_table, _I32, dev, "page_table"), max_pages, batch, 0), heads, dim)
 
 
 def mq_rope_kv_append(qkv: torch.Tensor, rope, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales,
@@ -333,24 +266,8 @@ def mq_rope_kv_append(qkv: torch.Tensor, rope, cu_rows, lens, page_table, k_code
     [T, q heads, head_dim] and, with V, into the cache (k_codes, v_codes
     [pages, kv heads, page size, head_dim], scales [pages, kv heads]).  rope:
     [positions, rot_dim] float32 (rope_table), None for rot_dim = 0."""
-    dev = _current(qkv, "qkv")
-    cache, batch, heads, dim = _kv_args(dev, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales)
-    T, q_heads, q_dim = q_out.shape
-    width = (q_heads + 2 * heads) * dim
-    if q_dim != dim or qkv.shape != (T, width):
-        raise ValueError("qkv [T, (q heads + 2 kv heads) head_dim] and q_out [T, q heads, head_dim] do not agree")
-    rope_ptr, positions = None, 0
-    if rope is not None:
-        positions, columns = rope.shape
-        rope_ptr = _addr(rope, _F32, dev, "rope")
-        if rot_dim is None:
-            rot_dim = columns
-        if columns != rot_dim:
-            raise ValueError("rope: [positions, rot_dim] expected")
-    status = (_lib or lib()).mq_rope_kv_append(
-        qkv.data_ptr(), T, _row_stride("qkv", qkv, width), q_heads, rope_ptr, positions, rot_dim or 0,
-        1 if interleaved else 0, cache, batch, _addr(q_out, _BF16, dev, "q_out"),
-        None if ws is None else _addr(ws, _U8, dev, "ws"), 0 if ws is None else ws.numel(), _stream_ptr(stream, dev))
+    status = (_calls or _load_calls()).append(qkv, rope, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales,
+                                              q_out, ws, rot_dim, interleaved, stream)
     if status:
         raise MQError(status, "mq_rope_kv_append")
 
@@ -365,14 +282,8 @@ def mq_kv_attention(q: torch.Tensor, cu_rows, lens, page_table, k_codes, v_codes
                     stream=None) -> None:
     """Causal attention of q [T, q heads, head_dim] (rows may be apart, e.g. a
     slice of a wider tensor) over the cache, into out of the same shape."""
-    dev = _current(q, "q")
-    cache, batch, heads, dim = _kv_args(dev, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales)
-    T, q_heads, q_dim = q.shape
-    if q_dim != dim or out.shape != q.shape:
-        raise ValueError("q and out [T, q heads, head_dim] do not agree with the cache")
-    status = (_lib or lib()).mq_kv_attention(
-        q.data_ptr(), T, _row_stride("q", q, q_heads * dim), q_heads, cache, batch, max_q, max_len, scale,
-        _addr(out, _BF16, dev, "out"), _addr(ws, _U8, dev, "ws"), ws.numel(), _stream_ptr(stream, dev))
+    status = (_calls or _load_calls()).attention(q, cu_rows, lens, page_table, k_codes, v_codes, k_scales, v_scales, out, ws,
+                                                 max_q, max_len, scale, stream)
     if status:
         raise MQError(status, "mq_kv_attention")
 
