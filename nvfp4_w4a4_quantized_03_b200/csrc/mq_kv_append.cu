@@ -132,12 +132,6 @@ __device__ __forceinline__ int page_exponent(float amax) {
     return max(KV_E_MIN, min(KV_E_MAX, e));
 }
 
-// Of each half of a pair: the larger of a and |b|; a NaN in b counts as nothing.
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ bool any_nan_bf16x2(const uint4& v) {
     uint32_t r;
     asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"

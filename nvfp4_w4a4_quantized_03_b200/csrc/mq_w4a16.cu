@@ -63,6 +63,12 @@ __device__ __forceinline__ uint32_t pack_f16(float hi, float lo) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// A bf16 pair times a power of two (exact above 2^-126), to f16.
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t x, uint32_t pow2) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(pow2));
+    return pack_f16(__uint_as_float(r & 0xFFFF0000u), __uint_as_float(r << 16));
+}
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -86,7 +92,7 @@ struct Shape {
     static constexpr int X_BYTES = 2 * MP * SUB * 2;     // two turns
     static constexpr int AHEAD = 4 / RT;                 // steps of W in registers
     static constexpr int TOKENS = MP / WARPS;            // tokens a warp converts
-    static constexpr int PER_SM = NT == 1 ? 3 : 2;       // blocks, by registers
+    static constexpr int PER_SM = 2;                     // blocks, by registers
     static constexpr int PART_BYTES = MP * ROWS * 4;
     static constexpr int SMEM = X_BYTES > PART_BYTES ? X_BYTES : PART_BYTES;
 };
@@ -103,10 +109,11 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     const int block = blockIdx.x / p.split;            // rows [block ROWS, ...)
     const int k_lo = (int)rank * p.slice, k_hi = min(p.K, k_lo + p.slice);
 
-    // W's rows of this block toward L2 before the wait for the previous grid:
-    // a prefetch leaves nothing visible
+    // the first columns of W's rows toward L2 before the wait for the previous
+    // grid (a prefetch leaves nothing visible; of the whole slice it took
+    // bandwidth from the loads: 18.3 -> 20.0 us for 1 x 24576 x 4096)
     if (tid < ROWS && block * ROWS + tid < p.N && k_hi > k_lo)
-        bulk_prefetch_l2(p.w_codes + (int64_t)(block * ROWS + tid) * (p.K / 2) + k_lo / 2, (k_hi - k_lo) / 2);
+        bulk_prefetch_l2(p.w_codes + (int64_t)(block * ROWS + tid) * (p.K / 2) + k_lo / 2, min(SUB, k_hi - k_lo) / 2);
 
     // the warp's tile in each atom of 128 rows: rows 4 warp + (r & 3) + 32 (r >> 2)
     const uint8_t* codes[RT][2];
@@ -171,30 +178,24 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
         for (int i = 0; i < BATCH; ++i) {
             const int m = warp + WARPS * (first + i);
             if (m >= p.M) break;
-            float top = 0.f;
+            uint32_t top = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t u[4] = {xw[i][h].x, xw[i][h].y, xw[i][h].z, xw[i][h].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+                const uint4& w = xw[i][h];
+                top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, w.x), w.y), w.z), w.w);
             }
-            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xFFFF0000u));
             const int e = max(e_run[first + i], (int)(bits >> 23) - 127 - 13);        // the maximum to [2^13, 2^14)
             if (lane == 0) {
                 s_ratio[turn][m] = exp2i(max(-126, e_run[first + i] - e));
                 s_up[m] = exp2i(e);
             }
             e_run[first + i] = e;
-            const float d = exp2i(-e);
+            const uint32_t d = cvt_bf16x2(exp2i(-e), exp2i(-e));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint4 w = xw[i][h];
-                uint4 f;
-                f.x = pack_f16(__uint_as_float(w.x & 0xFFFF0000u) * d, __uint_as_float(w.x << 16) * d);
-                f.y = pack_f16(__uint_as_float(w.y & 0xFFFF0000u) * d, __uint_as_float(w.y << 16) * d);
-                f.z = pack_f16(__uint_as_float(w.z & 0xFFFF0000u) * d, __uint_as_float(w.z << 16) * d);
-                f.w = pack_f16(__uint_as_float(w.w & 0xFFFF0000u) * d, __uint_as_float(w.w << 16) * d);
+                const uint4 f = make_uint4(to_f16x2(w.x, d), to_f16x2(w.y, d), to_f16x2(w.z, d), to_f16x2(w.w, d));
                 // as the fragments are read: [step][8 elements of a lane's 32][token][lane quarter]
                 const int v = h * 32 + lane;
                 *reinterpret_cast<uint4*>(smem + turn * (MP * SUB * 2) +
@@ -368,8 +369,16 @@ cudaError_t launch_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8
              (int)M, (int)N, (int)K, (int)scale_atom_cols(K), 0, 1};
     if (M <= 8) return launch<1, 1>(p, num_sms, stream);
     if (M <= 16) return launch<2, 1>(p, num_sms, stream);
-    if (M <= 32) return launch<4, 1>(p, num_sms, stream);
-    return launch<8, 1>(p, num_sms, stream);
+    // 32 tokens at a time: eight n-tiles do not fit the registers, and reading W
+    // a second time costs less (64 x 4096 x 12288: 98 us as one)
+    for (int64_t m = 0; m < M; m += 32) {
+        p.x = static_cast<const __nv_bfloat16*>(x) + m * K;
+        p.y = static_cast<__nv_bfloat16*>(y) + m * N;
+        p.M = (int)(M - m < 32 ? M - m : 32);
+        const cudaError_t e = launch<4, 1>(p, num_sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace mq
