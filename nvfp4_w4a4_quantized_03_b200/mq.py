@@ -12,6 +12,7 @@ index-computed access and TMA coordinate bounds-checked) is loaded instead.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -392,6 +393,125 @@ class MLPW4A4:
         """H [M, inter] as the last call left it in the workspace."""
         off = mq_linear_w4a4_workspace_bytes(M, self.K)
         return self._ws[off:off + M * self.inter * 2].view(torch.bfloat16).view(M, self.inter)
+
+
+class LinearW4A16:
+    """A linear layer y = x W^T whose activation stays in bf16 (decode steps of
+    at most 64 rows): W in NVFP4, quantized here or shared with a LinearW4A4."""
+
+    def __init__(self, weight):
+        if isinstance(weight, LinearW4A4):
+            weight = weight.w
+        if not isinstance(weight, QuantizedTensor):
+            assert weight.dtype == torch.bfloat16 and weight.is_cuda
+            weight = quantize(weight.contiguous())
+        self.w, self.N, self.K = weight, weight.rows, weight.K
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        M, K = x.shape
+        assert K == self.K
+        if out is None:
+            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+        mq_linear_w4a16(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, stream)
+        return out
+
+
+def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, scaling: dict | None = None,
+               device="cuda") -> torch.Tensor:
+    """[positions, rot_dim] float32: cos, then sin, of position * f_j, f_j =
+    theta^(-2 j / rot_dim), j < rot_dim / 2, with angles in 64 bits.
+
+    scaling, for contexts longer than a model was trained on:
+      {"kind": "linear", "factor": s}   f_j / s
+      {"kind": "yarn", "factor": s, "original": L, "beta_fast": 32, "beta_slow": 1}
+          f_j / s for pairs that turn less than beta_slow times within L
+          positions, f_j for those that turn more than beta_fast times, a
+          linear blend over j between, and cos and sin times 0.1 ln(s) + 1
+          (Peng et al., "YaRN: Efficient Context Window Extension of Large
+          Language Models", 2023, section 3)."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim: a positive even number expected")
+    j = torch.arange(rot_dim // 2, dtype=torch.float64)
+    f, size = theta ** (-2.0 * j / rot_dim), 1.0
+    if scaling is not None:
+        kind, s = scaling["kind"], float(scaling["factor"])
+        if kind == "linear":
+            f = f / s
+        elif kind == "yarn":
+            # the pair that turns `beta` times within L positions: f L = 2 pi beta
+            at = [rot_dim * math.log(scaling["original"] / (2 * math.pi * scaling.get(name, beta))) / (2 * math.log(theta))
+                  for name, beta in (("beta_fast", 32.0), ("beta_slow", 1.0))]
+            low, high = max(0, math.floor(at[0])), min(rot_dim - 1, math.ceil(at[1]))
+            ramp = ((j - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+            f = f / s * ramp + f * (1.0 - ramp)
+            size = 0.1 * math.log(s) + 1.0 if s > 1.0 else 1.0
+        else:
+            raise ValueError(f"scaling: kind 'linear' or 'yarn' expected, got {kind!r}")
+    f = f.to(device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.cat([angle.cos(), angle.sin()], 1) * size).float()
+
+
+class PagedKVCache:
+    """A pool of E4M3 pages (mq_kv_cache): k, v [pages, kv heads, page size,
+    head_dim], one power-of-two scale per (page, kv head).  Which page holds
+    what is the caller's page table."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, device):
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in "kv")
+        self.k_scale, self.v_scale = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in "kv")
+        self.page_size, self.kv_heads, self.head_dim = page_size, kv_heads, head_dim
+
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+
+class AttentionW4A4:
+    """The attention block of a decoder layer, from its input to its O linear:
+    QKV linear, rotary positions, append to the paged cache, attention, O
+    linear.  The weights are NVFP4; `precise` says whether the linears quantize
+    their activation (prefill, LinearW4A4) or not (decode, LinearW4A16, at most
+    64 rows).
+
+    w_qkv [(q heads + 2 kv heads) head_dim, hidden] (q, k, v rows in this
+    order), w_o [hidden, q heads * head_dim]; rope: rope_table(...)."""
+
+    def __init__(self, w_qkv: torch.Tensor, w_o: torch.Tensor, q_heads: int, kv_heads: int, head_dim: int,
+                 rope: torch.Tensor, interleaved: bool = False):
+        assert w_qkv.shape[0] == (q_heads + 2 * kv_heads) * head_dim and w_o.shape[1] == q_heads * head_dim
+        self.qkv, self.o = LinearW4A4(w_qkv), LinearW4A4(w_o)
+        self.qkv_precise, self.o_precise = LinearW4A16(self.qkv), LinearW4A16(self.o)
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.rope, self.interleaved = rope, interleaved
+        self._ws = None
+
+    def workspace(self, batch: int, max_q: int, max_len: int, device) -> torch.Tensor:
+        need = mq_kv_attention_workspace_bytes(batch, self.q_heads, self.kv_heads, self.head_dim, max_q, max_len)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = workspace(need, device)
+        return self._ws
+
+    def __call__(self, x: torch.Tensor, cache: PagedKVCache, cu_rows, lens, page_table, max_q: int, max_len: int,
+                 precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x [T, hidden]: the new tokens of the batch (mq_kv_batch of mq.h);
+        no sequence has more than max_q of them, or more than max_len tokens.
+        Rows that no sequence owns come out undefined."""
+        T = x.shape[0]
+        ws = self.workspace(page_table.shape[0], max_q, max_len, x.device)
+        qkv = (self.qkv_precise if precise else self.qkv)(x, stream=stream)
+        q = torch.empty(T, self.q_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
+        attended = torch.empty_like(q)
+        mq_rope_kv_append(qkv, self.rope, cu_rows, lens, page_table, *cache.tensors(), q, ws,
+                          interleaved=self.interleaved, stream=stream)
+        mq_kv_attention(q, cu_rows, lens, page_table, *cache.tensors(), attended, ws, max_q, max_len,
+                        self.head_dim ** -0.5, stream)
+        return (self.o_precise if precise else self.o)(attended.view(T, -1), out, stream)
+
+    def status(self, stream=None) -> int:
+        """The workspace's status word (mq_read_status): MQ_ERR_INVALID_ARG when
+        a length, position or page number was outside the tables."""
+        return mq_read_status(self._ws, stream)
 
 
 # -- the allocation-free variant (library-owned scratch) ---------------------

@@ -6,6 +6,10 @@ to NVFP4 inside each call and multiplied with the layer's pre-quantized
 weight.  The norms, attention and SwiGLU between the linears are not part of
 this path, so each projection reads a fixed activation of its own shape.
 
+With `attention=True` the attention stands between the QKV and the O linear:
+rotary positions, every layer's K and V appended to its paged E4M3 cache, causal
+attention of the prompt over it; the O linear reads its output.
+
 With `mlp=True` each layer runs the QKV and O linears and then its MLP as
 one mq_mlp_w4a4 call: the gate/up GEMM with SwiGLU in its epilogue, H
 quantized with its own tensor scale, and the down GEMM; the MLP reads the
@@ -29,8 +33,10 @@ from . import inputs, mq
 
 class PrefillSequence:
     def __init__(self, layers: int, tokens: int, device, weight_seed: int = 1000, act_seed: int = 2000,
-                 projections=inputs.QWEN3_8B_PROJECTIONS, mlp: bool = False):
+                 projections=inputs.QWEN3_8B_PROJECTIONS, mlp: bool = False, attention: bool = False,
+                 kv_heads: int = 8, head_dim: int = 128, page_size: int = 64):
         self.layers, self.tokens, self.device = layers, tokens, device
+        self.attention = attention
         self.projections = projections
         self.mlp = mlp
         names = [p.name for p in projections]
@@ -61,9 +67,24 @@ class PrefillSequence:
         if mlp:
             nbytes = max(nbytes, mq.mq_mlp_w4a4_workspace_bytes(tokens, projections[self.i_gu].K, self.inter))
         self.ws = mq.workspace(nbytes, device)
+        if attention:
+            self.i_qkv, self.i_o = names.index("qkv"), names.index("o")
+            q_heads = projections[self.i_o].K // head_dim
+            assert projections[self.i_qkv].N == (q_heads + 2 * kv_heads) * head_dim
+            pages = -(-tokens // page_size)
+            self.q = torch.empty(tokens, q_heads, head_dim, dtype=torch.bfloat16, device=device)
+            self.x[self.i_o] = torch.empty(tokens, q_heads * head_dim, dtype=torch.bfloat16, device=device)
+            self.rope = mq.rope_table(tokens, head_dim, theta=1e6, device=device)
+            self.caches = [mq.PagedKVCache(pages, page_size, kv_heads, head_dim, device) for _ in range(layers)]
+            i32 = dict(dtype=torch.int32, device=device)
+            self.batch = (torch.tensor([0, tokens], **i32), torch.tensor([tokens], **i32),
+                          torch.arange(pages, **i32)[None])
+            self.ws_attention = mq.workspace(
+                mq.mq_kv_attention_workspace_bytes(1, q_heads, kv_heads, head_dim, tokens, tokens), device)
         self.graph = None
 
     def flops(self) -> float:
+        """Of the linears."""
         return 2.0 * self.tokens * self.layers * sum(p.N * p.K for p in self.projections)
 
     def run(self, stream=None) -> None:
@@ -80,10 +101,16 @@ class PrefillSequence:
                     continue
                 else:
                     mq.mq_linear_w4a4(self.x[i], q.codes, q.scales, q.alpha, p.N, self.y[i], self.ws, stream)
+                if self.attention and i == self.i_qkv:
+                    cache = self.caches[layer].tensors()
+                    mq.mq_rope_kv_append(self.y[i], self.rope, *self.batch, *cache, self.q, self.ws_attention, stream=stream)
+                    mq.mq_kv_attention(self.q, *self.batch, *cache, self.x[self.i_o].view(self.q.shape),
+                                       self.ws_attention, self.tokens, self.tokens, self.q.shape[2] ** -0.5, stream)
 
     def launches(self) -> int:
-        """Kernel launches of one run(): two per linear, five per MLP."""
-        return self.layers * (2 * (len(self.projections) - 2) + 5 if self.mlp else 2 * len(self.projections))
+        """Kernel launches of one run(): two per linear, five per MLP, two for the append and the attention."""
+        return self.layers * ((2 * (len(self.projections) - 2) + 5 if self.mlp else 2 * len(self.projections)) +
+                              (2 if self.attention else 0))
 
     def capture(self) -> None:
         """Record run() in a CUDA graph (after an eager pass, so that every
@@ -104,4 +131,7 @@ class PrefillSequence:
         self.graph.replay()
 
     def status(self) -> int:
-        return mq.mq_read_status(self.ws)
+        status = mq.mq_read_status(self.ws)
+        if status == mq.MQ_OK and self.attention:
+            status = mq.mq_read_status(self.ws_attention)
+        return status
