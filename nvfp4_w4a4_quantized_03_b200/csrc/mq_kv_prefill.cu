@@ -26,9 +26,13 @@
 // a tile's own chain (products 1420 cycles, scores and maximum 550, weights
 // 1750, hand-overs) is ~4000, and two tiles in turn leave either pipe about
 // half idle: 8192-token prompt, 32 heads of 128: 0.60 ms, 920 TFLOP/s.
-// Measured against this form and dropped: two threads per row (0.69 ms), the
-// weights under the last block's maximum, computed again where it rose (0.65
-// ms), a quarter of the exponentials as polynomials on the FMA pipe (no change).
+// Measured against this form and dropped (same prompt): two threads per row
+// (0.69 ms), the weights under the last block's maximum, computed again where it
+// rose (0.65 ms), an issuer of its own for each tile (0.73 ms; 0.63 ms with the
+// tiles taking turns), Q in tensor memory at D = 64 (3% slower).  With neither
+// softmax nor conversions the products run at 2050 cycles per block, with the
+// conversions at 3350: the converters' stores and the tensor pipe's reads share
+// the bandwidth of shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -126,6 +130,25 @@ __device__ __forceinline__ float ex2v(float x) {
     float y;
     asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// 2^x of a pair, x <= 120, on the FMA pipe: x = i + f with i the nearest integer
+// (it appears in the low bits of x + 1.5 * 2^23), 2^f = 1 + f (c1 + f (c2 + f (c3 + f c4)))
+// with coefficients fitted here to the least largest relative error on
+// [-1/2, 1/2], 2^-18.4; i goes into the exponent.  Below 2^-126 the result
+// runs out towards 0, which it is from -127 on (-inf too).
+__device__ __forceinline__ void exp2_pair(float& x, float& y) {
+    const uint64_t v = pack2(fmaxf(x, -127.f), fmaxf(y, -127.f));
+    const uint64_t t = add2(v, pack2(12582912.f, 12582912.f));
+    const uint64_t f = fma2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), v);
+    uint64_t q = fma2(f, pack2(0x1.3a02ccp-7f, 0x1.3a02ccp-7f), pack2(0x1.c9fc46p-5f, 0x1.c9fc46p-5f));
+    q = fma2(f, q, pack2(0x1.ec0378p-3f, 0x1.ec0378p-3f));
+    q = fma2(f, q, pack2(0x1.62e12cp-1f, 0x1.62e12cp-1f));
+    q = fma2(f, q, pack2(1.f, 1.f));
+    float a, b, c, d;
+    unpack2(t, a, b);
+    unpack2(q, c, d);
+    x = __uint_as_float(__float_as_uint(c) + (__float_as_uint(a) << 23));
+    y = __uint_as_float(__float_as_uint(d) + (__float_as_uint(b) << 23));
 }
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
     float r;
@@ -368,8 +391,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
                         for (int i = 0; i < 8; ++i) {
                             float w0, w1;
                             unpack2(u[g & 1][i], w0, w1);
-                            e[g & 1][2 * i] = ex2v(w0);
-                            e[g & 1][2 * i + 1] = ex2v(w1);
+                            // D = 64: three pairs of eight on the FMA pipe (448 ->
+                            // 425 us for an 8192-token prompt of 28 heads; at
+                            // D = 128, where the products are longer, no gain)
+                            if (D == 64 && (i == 1 || i == 4 || i == 6)) {
+                                exp2_pair(w0, w1);
+                            } else {
+                                w0 = ex2v(w0);
+                                w1 = ex2v(w1);
+                            }
+                            e[g & 1][2 * i] = w0;
+                            e[g & 1][2 * i + 1] = w1;
                         }
                         if (g + 1 < GROUPS) exponents(g + 1);
                     }

@@ -142,7 +142,8 @@ def attention_plain(bt, q, scale):
     In units of 2^-24 = u (half a binary32 step, relative): a score s = scale sum q k is a binary32 sum of D exact
     products, in any order, truncated or rounded (2 u each): off by at most 2 (D + 4) u S, S = scale sum |q k|, the
     factors and the subtraction of the maximum included with |s| <= S; a weight's relative error is that, twice
-    (its row's maximum), plus 2^-12 (its rounding to f16) and 2^-20 (the exponential, merges).  Sums over L keys
+    (its row's maximum), plus 2^-12 (its rounding to f16) and 2^-18 (the exponential: a polynomial
+    within 2^-18.4, or ex2.approx within 2^-22; merges).  Sums over L keys
     add 2 L u.  A weight below f16's normal range is off by 2^-25 where the largest is at least 2^6, times a code
     of at most 448 under the largest scale.  q in f16 is exact above 2^-38 of its row's maximum, which the
     subnormal bound covers (D 2^-38 S)."""
@@ -170,7 +171,7 @@ def attention_plain(bt, q, scale):
                 w = (s - m).exp()
                 w /= w.sum(1, keepdim=True).clamp(min=1e-300)
                 S = (x.abs() @ k.abs().T * scale).masked_fill(hidden, 0).amax(1, keepdim=True)
-                rel = 2 * (2 * (D + 4) * u + D * 2.0 ** -38) * S + 2.0 ** -12 + 2.0 ** -20 + 4 * length * u
+                rel = 2 * (2 * (D + 4) * u + D * 2.0 ** -38) * S + 2.0 ** -12 + 2.0 ** -18 + 4 * length * u
                 out[r0:r0 + n, h * G + g] = w @ v
                 bound[r0:r0 + n, h * G + g] = 2 * rel * (w @ v.abs()) + length * 2.0 ** -31 * 448 * top_scale
     return out, bound
