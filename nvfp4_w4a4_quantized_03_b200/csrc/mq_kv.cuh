@@ -95,25 +95,32 @@ __device__ __forceinline__ void kv_join(const KvAttendParams& p, float* part, in
     constexpr int V4 = D / 4;
     const int64_t step = (int64_t)rows_cap * D;
     const float2* ml = reinterpret_cast<const float2*>(kv_part_ml<D>(p, part, rows_cap));
-    const int lane = tid % 32;
-    // each row's maximum and the chunks' weights 2^(M - max) / sum: a warp per row
-    for (int r = tid / 32; r < nrows; r += threads / 32) {
+    // each row's maximum and the chunks' weights 2^(M - max) / sum: by a warp per
+    // row where rows are few, by a thread per row where they are many
+    const int width = nrows <= 64 ? 32 : 1, lane = tid % width;
+    for (int r = tid / width; r < nrows; r += threads / width) {
         float top = -INFINITY;
-        for (int c = lane; c < chunks; c += 32) top = fmaxf(top, __ldcg(&ml[c * rows_cap + r].x));
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += width) top = fmaxf(top, __ldcg(&ml[c * rows_cap + r].x));
+        if (width == 32) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
         float lsum = 0.f;
-        for (int c = lane; c < chunks; c += 32) {
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += width) {
             const float2 v = __ldcg(&ml[c * rows_cap + r]);
             const float f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
             weights[r * chunks + c] = f;
             lsum = __fmaf_rn(v.y, f, lsum);
         }
+        if (width == 32) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+            for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+        }
         // a row that saw nothing: zero
         const float inv = lsum > 0.f || lsum != lsum ? __fdiv_rn(1.f, lsum) : 0.f;
-        for (int c = lane; c < chunks; c += 32) weights[r * chunks + c] *= inv;
+        for (int c = lane; c < chunks; c += width) weights[r * chunks + c] *= inv;
     }
     __syncthreads();
     for (int i = tid; i < nrows * V4; i += threads) {

@@ -22,7 +22,7 @@ struct KvPlan {
 
 inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
                       int64_t max_len) {
-    constexpr int64_t TICKETS = 592;
+    constexpr int64_t SMS = 148, TICKETS = 4 * SMS;
     KvPlan p{};
     const int64_t rows = max_q * (q_heads / kv_heads);
     p.prefill = rows > 16;
@@ -30,15 +30,18 @@ inline KvPlan kv_plan(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t 
     p.block_rows = p.prefill ? 256 : 8 * p.nt;
     p.row_tiles = (rows + p.block_rows - 1) / p.block_rows;
     p.cells = batch * p.row_tiles * kv_heads;
-    // one chunk where the cells fill the device (one block of the tcgen05 form
-    // per SM; four of the other); else enough chunks to do
-    // so, of 128 (256) tokens at least and of 1024 at most, but never more than
-    // 128 (64) of them: the last block to finish a cell reads them all
-    const int64_t fill = p.prefill ? 148 : 592;
+    // One chunk where the cells fill the device.  Else enough chunks to do so:
+    // of the tcgen05 form (one block per SM) as many as run at once, of 512
+    // tokens at least (the last block to finish a cell reads back 128 KB per
+    // chunk); of the other (four blocks per SM) of 128 to 1024 tokens, but
+    // never more than 128 of them.
     int64_t c = std::max<int64_t>(max_len, 128);
-    if (p.cells < fill) {
-        const int64_t want = (p.cells * max_len + fill - 1) / fill, most = p.prefill ? 64 : 128;
-        c = std::max({std::min<int64_t>(want, 1024), (max_len + most - 1) / most, (int64_t)(p.prefill ? 256 : 128)});
+    if (p.prefill && p.cells < SMS) {
+        const int64_t n = std::min<int64_t>(SMS / p.cells, 64);
+        c = std::max<int64_t>((max_len + n - 1) / n, 512);
+    } else if (!p.prefill && p.cells < TICKETS) {
+        const int64_t want = (p.cells * max_len + TICKETS - 1) / TICKETS;
+        c = std::max({std::min<int64_t>(want, 1024), (max_len + 127) / 128, (int64_t)128});
     }
     p.chunk_tokens = (c + 127) / 128 * 128;
     if (!p.prefill) p.chunk_tokens = (c + 63) / 64 * 64;
