@@ -72,7 +72,7 @@ __device__ __forceinline__ void load_codes(uint32_t (&w)[N], const uint8_t* p) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) k_kv_attend(Params p) {
+__global__ void __launch_bounds__(THREADS, NT == 1 ? (D == 64 ? 5 : 4) : (D == 64 ? 4 : 3)) k_kv_attend(Params p) {
     constexpr int ROWS = 8 * NT;
     constexpr int KH = D / 64;               // 16-byte pieces of a K row per lane
     constexpr int VW = D / 32;               // words of a V row per lane
