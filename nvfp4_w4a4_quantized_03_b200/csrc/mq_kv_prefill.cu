@@ -25,7 +25,7 @@
 // tensor pipe at D = 128 and their 32768 exponentials 2048 cycles of the SFU;
 // a tile's own chain (products 1420 cycles, scores and maximum 550, weights
 // 1750, hand-overs) is ~4000, and two tiles in turn leave either pipe about
-// half idle: 8192-token prompt, 32 heads of 128: 0.60 ms, 920 TFLOP/s.
+// half idle: 8192-token prompt, 32 heads of 128: 0.61 ms, 900 TFLOP/s.
 // Measured against this form and dropped (same prompt): two threads per row
 // (0.69 ms), the weights under the last block's maximum, computed again where it
 // rose (0.65 ms), an issuer of its own for each tile (0.73 ms; 0.63 ms with the

@@ -9,17 +9,22 @@
 // left.  So the f16 products of mma.m16n8k16 are those of the exact operands;
 // sums are binary32, with one rounding to bf16 at the end.
 // (bf16 operands would spare x its conversion, but an E2M1 pair goes to f16 in
-// one instruction and to bf16 in five: measured 21.5 us against the present
-// figure for 5 x 24576 x 4096.)
+// one instruction and to bf16 in five.)
 //
-// Bound: the weight is read once (0.5625 bytes per element).  A block holds 128
-// or 256 rows of W and one slice of K, the blocks of a cluster the slices of
-// the same rows; a block's partial sums are added through distributed shared
-// memory in rank order.  Each lane reads 16 bytes (32 elements, two scale
-// blocks) of a row at a time, four steps ahead, and the order of K inside a
-// fragment is free, so what a lane loads is what it multiplies.  A warp's 16
-// rows are four runs of four, 32 rows apart: that is where the stored scales
-// of one 64-byte piece belong, so no scale sector is read twice.
+// Bound: the weight is read once (0.5625 bytes per element), but its decoding
+// keeps up with memory only just: ~180 instructions per 16 rows x 128 columns
+// of a warp, 2 cycles each on the ALU.  Measured: 1 x 4096 x 4096 5.1 us, 1 x
+// 6144 x 4096 6.8, 1 x 24576 x 4096 17.9 (3.2 TB/s; 14.6 with the arithmetic
+// left out, 12.3 with the loads left out), 5 x 24576 x 4096 19.3, 32 x 4096 x
+// 12288 22.5.  A block holds 128 rows of W and one slice of K, the blocks of a
+// cluster the slices of the same rows; a block's partial sums are added through
+// distributed shared memory in rank order.  Each lane reads 16 bytes (32
+// elements, two scale blocks) of a row at a time, four steps ahead, and the
+// order of K inside a fragment is free, so what a lane loads is what it
+// multiplies.  A warp's 16 rows are four runs of four, 32 rows apart: that is
+// where the stored scales of one 64-byte piece belong, so no scale sector is
+// read twice.  Dropped: one persistent block per SM with rings of its own for
+// every warp (17.3 and 19.0 us for 1 and 5 x 24576 x 4096, slower below).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -86,20 +91,20 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
-template <int NT, int RT>
+template <int NT>
 struct Shape {
-    static constexpr int MP = 8 * NT, ROWS = 128 * RT;
+    static constexpr int MP = 8 * NT, ROWS = 128;
     static constexpr int X_BYTES = 2 * MP * SUB * 2;     // two turns
-    static constexpr int AHEAD = 4 / RT;                 // steps of W in registers
+    static constexpr int AHEAD = 4;                      // steps of W in registers
     static constexpr int TOKENS = MP / WARPS;            // tokens a warp converts
     static constexpr int PER_SM = 2;                     // blocks, by registers
     static constexpr int PART_BYTES = MP * ROWS * 4;
     static constexpr int SMEM = X_BYTES > PART_BYTES ? X_BYTES : PART_BYTES;
 };
 
-template <int NT, int RT>
-__global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16(Params p) {
-    using S = Shape<NT, RT>;
+template <int NT>
+__global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM) k_linear_w4a16(Params p) {
+    using S = Shape<NT>;
     constexpr int MP = S::MP, ROWS = S::ROWS, AHEAD = S::AHEAD, TOKENS = S::TOKENS;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_ratio[2][MP];                   // what a token's sums so far are to be multiplied with
@@ -115,19 +120,16 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     if (tid < ROWS && block * ROWS + tid < p.N && k_hi > k_lo)
         bulk_prefetch_l2(p.w_codes + (int64_t)(block * ROWS + tid) * (p.K / 2) + k_lo / 2, min(SUB, k_hi - k_lo) / 2);
 
-    // the warp's tile in each atom of 128 rows: rows 4 warp + (r & 3) + 32 (r >> 2)
-    const uint8_t* codes[RT][2];
-    const uint8_t* scales[RT][2];
+    // the warp's tile of the block's 128 rows: rows 4 warp + (r & 3) + 32 (r >> 2)
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = g + 8 * h, in = warp * 4 + (r & 3);
-            const int atom = min(block * RT + i, (p.N + 127) / 128 - 1);
-            const int row = min(block * ROWS + i * 128 + in + 32 * (r >> 2), p.N - 1);    // behind N: read, not written
-            codes[i][h] = p.w_codes + (int64_t)row * (p.K / 2) + k_lo / 2 + t * 16;
-            scales[i][h] = p.w_scales + ((int64_t)atom * p.katoms + k_lo / 64 + (t >> 1)) * 512 + in * 16 + (r >> 2) * 4 + 2 * (t & 1);
-        }
+    for (int h = 0; h < 2; ++h) {
+        const int r = g + 8 * h, in = warp * 4 + (r & 3);
+        const int row = min(block * ROWS + in + 32 * (r >> 2), p.N - 1);                  // behind N: read, not written
+        codes[h] = p.w_codes + (int64_t)row * (p.K / 2) + k_lo / 2 + t * 16;
+        scales[h] = p.w_scales + ((int64_t)block * p.katoms + k_lo / 64 + (t >> 1)) * 512 + in * 16 + (r >> 2) * 4 + 2 * (t & 1);
+    }
     // K is a multiple of 64: where the slice ends in half a step, its upper
     // lanes read what the lower ones do; X is zero there
     const int steps = (k_hi - k_lo + STEP - 1) / STEP;
@@ -135,8 +137,8 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     pdl_launch_dependents();
     pdl_wait();
 
-    uint4 cw[AHEAD][RT][2];
-    uint16_t sw[AHEAD][RT][2];
+    uint4 cw[AHEAD][2];
+    uint16_t sw[AHEAD][2];
     auto load = [&](int a, int step, int at) {             // `at`: steps from where the pointers stand
         if (step < steps) {
             int ch = at * (STEP / 2), sh = at * (STEP / 64 * 512);
@@ -145,12 +147,10 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
                 sh -= 512;
             }
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    cw[a][i][h] = load_stream(codes[i][h] + ch);
-                    sw[a][i][h] = *reinterpret_cast<const uint16_t*>(scales[i][h] + sh);
-                }
+            for (int h = 0; h < 2; ++h) {
+                cw[a][h] = load_stream(codes[h] + ch);
+                sw[a][h] = *reinterpret_cast<const uint16_t*>(scales[h] + sh);
+            }
         }
     };
 #pragma unroll
@@ -159,24 +159,23 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
     // X, 512 columns at a time: a warp converts tokens warp, warp + 8, ..., 16
     // elements per lane, under the largest exponent of the token so far
     int e_run[TOKENS];
-    constexpr int BATCH = TOKENS < 4 ? TOKENS : 4;         // tokens held in registers, loaded a turn ahead if that is all
-    uint4 xw[BATCH][2];
+    uint4 xw[TOKENS][2];
 #pragma unroll
     for (int i = 0; i < TOKENS; ++i) e_run[i] = -113;
-    auto load_x = [&](int k0, int first) {
+    auto load_x = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
+        for (int i = 0; i < TOKENS; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int m = warp + WARPS * (first + i), k = k0 + h * 256 + lane * 8;
+                const int m = warp + WARPS * i, k = k0 + h * 256 + lane * 8;
                 xw[i][h] = make_uint4(0, 0, 0, 0);
                 if (m < p.M && k < k_hi) xw[i][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K + k));
             }
     };
-    auto convert = [&](int turn, int first) {
+    auto convert = [&](int turn) {
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int m = warp + WARPS * (first + i);
+        for (int i = 0; i < TOKENS; ++i) {
+            const int m = warp + WARPS * i;
             if (m >= p.M) break;
             uint32_t top = 0;
 #pragma unroll
@@ -185,12 +184,12 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
                 top = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(top, w.x), w.y), w.z), w.w);
             }
             const uint32_t bits = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xFFFF0000u));
-            const int e = max(e_run[first + i], (int)(bits >> 23) - 127 - 13);        // the maximum to [2^13, 2^14)
+            const int e = max(e_run[i], (int)(bits >> 23) - 127 - 13);        // the maximum to [2^13, 2^14)
             if (lane == 0) {
-                s_ratio[turn][m] = exp2i(max(-126, e_run[first + i] - e));
+                s_ratio[turn][m] = exp2i(max(-126, e_run[i] - e));
                 s_up[m] = exp2i(e);
             }
-            e_run[first + i] = e;
+            e_run[i] = e;
             const uint32_t d = cvt_bf16x2(exp2i(-e), exp2i(-e));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -203,25 +202,18 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
             }
         }
     };
-    load_x(k_lo, 0);
+    load_x(k_lo);
 
-    float acc[RT][NT][4];
+    float acc[NT][4];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 
     int turn = 0;
     for (int k0 = k_lo, step0 = 0; k0 < k_hi; k0 += SUB, step0 += STEPS, turn ^= 1) {
         // Two turns of shared memory and one barrier: whoever writes a turn has
         // passed the barrier behind which the other one was read last.
-        convert(turn, 0);
-#pragma unroll
-        for (int first = BATCH; first < TOKENS; first += BATCH) {
-            load_x(k0, first);
-            convert(turn, first);
-        }
-        if (k0 + SUB < k_hi) load_x(k0 + SUB, 0);
+        convert(turn);
+        if (k0 + SUB < k_hi) load_x(k0 + SUB);
         __syncthreads();
         if (k0 > k_lo) {
 #pragma unroll
@@ -229,11 +221,8 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float r = s_ratio[turn][n * 8 + 2 * t + e];
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        acc[i][n][e] *= r;
-                        acc[i][n][e + 2] *= r;
-                    }
+                    acc[n][e] *= r;
+                    acc[n][e + 2] *= r;
                 }
         }
         const uint8_t* xs = smem + turn * (MP * SUB * 2);
@@ -241,65 +230,55 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
         for (int s = 0; s < STEPS; ++s) {
             if (step0 + s >= steps) break;
             const int a = s % AHEAD;
-            uint32_t sf[RT][2][2];
+            uint32_t sf[2][2];
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t v = cvt_e4m3x2_to_f16x2(sw[a][i][h]);
-                    sf[i][h][0] = __byte_perm(v, v, 0x1010);
-                    sf[i][h][1] = __byte_perm(v, v, 0x3232);
-                }
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t v = cvt_e4m3x2_to_f16x2(sw[a][h]);
+                sf[h][0] = __byte_perm(v, v, 0x1010);
+                sf[h][1] = __byte_perm(v, v, 0x3232);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {              // words of eight codes; scale block j / 2 of the lane's two
                 uint4 b[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     b[n] = *reinterpret_cast<const uint4*>(xs + (((s * 4 + j) * MP + n * 8 + g) * 4 + t) * 16);
+                const uint4 &c0 = cw[a][0], &c1 = cw[a][1];
+                const uint32_t w0 = j == 0 ? c0.x : j == 1 ? c0.y : j == 2 ? c0.z : c0.w;
+                const uint32_t w1 = j == 0 ? c1.x : j == 1 ? c1.y : j == 2 ? c1.z : c1.w;
+                uint32_t h0[4], h1[4];
+                decode8(w0, h0);
+                decode8(w1, h1);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const uint4 &c0 = cw[a][i][0], &c1 = cw[a][i][1];
-                    const uint32_t w0 = j == 0 ? c0.x : j == 1 ? c0.y : j == 2 ? c0.z : c0.w;
-                    const uint32_t w1 = j == 0 ? c1.x : j == 1 ? c1.y : j == 2 ? c1.z : c1.w;
-                    uint32_t h0[4], h1[4];
-                    decode8(w0, h0);
-                    decode8(w1, h1);
+                for (int q = 0; q < 4; ++q) {
+                    h0[q] = mul_f16x2(h0[q], sf[0][j >> 1]);
+                    h1[q] = mul_f16x2(h1[q], sf[1][j >> 1]);
+                }
+                const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        h0[q] = mul_f16x2(h0[q], sf[i][0][j >> 1]);
-                        h1[q] = mul_f16x2(h1[q], sf[i][1][j >> 1]);
-                    }
-                    const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_f16(acc[i][n], a0, b[n].x, b[n].y);
-                        mma_f16(acc[i][n], a1, b[n].z, b[n].w);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    mma_f16(acc[n], a0, b[n].x, b[n].y);
+                    mma_f16(acc[n], a1, b[n].z, b[n].w);
                 }
             }
             load(a, step0 + s + AHEAD, s + AHEAD);
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                codes[i][h] += SUB / 2;
-                scales[i][h] += SUB / 64 * 512;
-            }
+        for (int h = 0; h < 2; ++h) {
+            codes[h] += SUB / 2;
+            scales[h] += SUB / 64 * 512;
+        }
     }
     // acc: rows g (0, 1) and g + 8 (2, 3) of a tile, tokens 2t and 2t + 1, to [token][row of the block]
     __syncthreads();
     float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = n * 8 + 2 * t + (e & 1), r = g + 8 * (e >> 1);
-                if (m < p.M)
-                    part[m * ROWS + i * 128 + warp * 4 + (r & 3) + 32 * (r >> 2)] = k_hi > k_lo ? acc[i][n][e] * s_up[m] : 0.f;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int m = n * 8 + 2 * t + (e & 1), r = g + 8 * (e >> 1);
+            if (m < p.M) part[m * ROWS + warp * 4 + (r & 3) + 32 * (r >> 2)] = k_hi > k_lo ? acc[n][e] * s_up[m] : 0.f;
+        }
     if (p.split > 1)
         cluster_sync();
     else
@@ -323,15 +302,15 @@ __global__ void __launch_bounds__(THREADS, Shape<NT, RT>::PER_SM) k_linear_w4a16
 
 MQ_DEBUG_READER(debug_hits_w4a16)
 
-template <int NT, int RT>
+template <int NT>
 cudaError_t launch(Params p, int num_sms, cudaStream_t stream) {
-    using S = Shape<NT, RT>;
+    using S = Shape<NT>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     const int d = dev < 64 ? dev : 63;
     if (!attr_set[d]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_w4a16<NT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(k_linear_w4a16<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
         attr_set[d] = true;
     }
@@ -356,7 +335,7 @@ cudaError_t launch(Params p, int num_sms, cudaStream_t stream) {
     set_pdl_attr(attr, &nattr);
     cfg.attrs = attr;
     cfg.numAttrs = nattr;
-    return cudaLaunchKernelEx(&cfg, k_linear_w4a16<NT, RT>, p);
+    return cudaLaunchKernelEx(&cfg, k_linear_w4a16<NT>, p);
 }
 
 }  // namespace w4a16
@@ -367,15 +346,15 @@ cudaError_t launch_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8
     using namespace w4a16;
     Params p{static_cast<const __nv_bfloat16*>(x), w_codes, w_scales, alpha_w, static_cast<__nv_bfloat16*>(y),
              (int)M, (int)N, (int)K, (int)scale_atom_cols(K), 0, 1};
-    if (M <= 8) return launch<1, 1>(p, num_sms, stream);
-    if (M <= 16) return launch<2, 1>(p, num_sms, stream);
+    if (M <= 8) return launch<1>(p, num_sms, stream);
+    if (M <= 16) return launch<2>(p, num_sms, stream);
     // 32 tokens at a time: eight n-tiles do not fit the registers, and reading W
     // a second time costs less (64 x 4096 x 12288: 98 us as one)
     for (int64_t m = 0; m < M; m += 32) {
         p.x = static_cast<const __nv_bfloat16*>(x) + m * K;
         p.y = static_cast<__nv_bfloat16*>(y) + m * N;
         p.M = (int)(M - m < 32 ? M - m : 32);
-        const cudaError_t e = launch<4, 1>(p, num_sms, stream);
+        const cudaError_t e = launch<4>(p, num_sms, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
