@@ -274,7 +274,7 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  *   qkv    : device bf16 [T, row_stride], row_stride >= (q_heads + 2 kv_heads)
  *            head_dim, a multiple of 8
  *   rope   : device float [max_pos][rot_dim], 16-byte aligned
- *   q_out  : device bf16 [T, q_heads, head_dim], written
+ *   q_out  : device bf16 [T, q_heads, head_dim], written; it may not overlap qkv
  *   ws     : optional workspace (256-byte header) whose status word takes
  *            MQ_ERR_INVALID_ARG when a position, a page number or a length is
  *            outside the tables: what it concerns is not written
@@ -300,7 +300,8 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  *             head_dim, max_q, max_len) bytes, 256-byte aligned, zero-filled
  *             before its first use and used by mq_kv_attention alone (calls
  *             of any sizes may follow one another on it); calls sharing it
- *             must not overlap on the GPU
+ *             must not overlap on the GPU.  The size is 0 for sizes that
+ *             the call refuses.
  */
 typedef struct mq_kv_cache {
     uint8_t *k_codes;

@@ -63,14 +63,15 @@ __device__ __forceinline__ uint32_t pack_f16(float hi, float lo) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// 16 or 8 bytes of codes, streamed: the cache is larger than L2 in earnest
+// 16 or 8 bytes of codes, streamed: the cache is larger than L2 in earnest (a
+// plain load: the append before it may still have been writing when this grid began)
 template <int N>
 __device__ __forceinline__ void load_codes(uint32_t (&w)[N], const uint8_t* p) {
     if constexpr (N == 4) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
     } else {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     }
 }
 
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? (D == 64 ? 5 : 4) : (D == 6
     id /= p.kv_heads;
     const int tile = p.row_tiles - 1 - id % p.row_tiles, b = id / p.row_tiles;
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
-    const int64_t len = p.lens[b];
+    const int64_t len = max(p.lens[b], 0);
     const int page_tokens = 1 << p.page_log2;
     if (n <= 0) return;
     // lengths that the call's arguments or the table do not cover: the rows stay as they were
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? (D == 64 ? 5 : 4) : (D == 6
     // The warp's steps of 16 keys: the page of the step after the next is
     // looked up while the codes and scales of the next are on their way.
     const int* table = p.table + (int64_t)b * p.max_pages;
-    auto page_of = [&](int tok0) { return tok0 < k1 ? __ldg(table + (tok0 >> p.page_log2)) : -1; };
+    auto page_of = [&](int tok0) { return tok0 < k1 ? table[tok0 >> p.page_log2] : -1; };
     int page = page_of(k0 + warp * STEP);
 
     // Q: row g of each n-tile, the d that the K fragments hold: 16 t .. 16 t + 15 (+ 64)
@@ -187,8 +188,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? (D == 64 ? 5 : 4) : (D == 6
         if (!valid && p.status && lane == 0) atomicExch(p.status, MQ_ERR_INVALID_ARG);
         const int64_t cell = valid ? (int64_t)page * p.kv_heads + head : 0;
         base = ((cell << p.page_log2) + (tok0 & (page_tokens - 1))) * D;
-        sk = __ldg(p.k_scales + cell);
-        sv = __ldg(p.v_scales + cell);
+        sk = p.k_scales[cell];
+        sv = p.v_scales[cell];
         const uint8_t* src = p.k_codes + base + g * D + t * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i)

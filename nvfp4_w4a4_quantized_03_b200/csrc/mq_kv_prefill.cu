@@ -157,7 +157,7 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
 }
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 template <int D>
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     id /= p.kv_heads;
     const int b = id % p.batch, tile = p.row_tiles - 1 - id / p.batch;
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
-    const int64_t len = p.lens[b];
+    const int64_t len = max(p.lens[b], 0);
     const int page_tokens = 1 << p.page_log2;
     if (n <= 0) return;
     if (c0 < 0 || (int64_t)c0 + n > p.T || n > p.max_q || len > p.max_len || len > p.max_pages << p.page_log2) {

@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t x, uint32_t pow2) {
 }
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM) k_linear_w4a16(Par
             for (int h = 0; h < 2; ++h) {
                 const int m = warp + WARPS * i, k = k0 + h * 256 + lane * 8;
                 xw[i][h] = make_uint4(0, 0, 0, 0);
-                if (m < p.M && k < k_hi) xw[i][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K + k));
+                if (m < p.M && k < k_hi) xw[i][h] = *reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.K + k);
             }
     };
     auto convert = [&](int turn) {
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::PER_SM) k_linear_w4a16(Par
     else
         __syncthreads();
     // the cluster's blocks finish a share of the outputs each, partial sums added in rank order
-    const float alpha = __ldg(p.alpha);
+    const float alpha = *p.alpha;
     const float* peer[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) peer[q] = q < p.split ? map_shared_rank(part, (uint32_t)q) : part;

@@ -484,11 +484,12 @@ class AttentionW4A4:
         self.qkv_precise, self.o_precise = LinearW4A16(self.qkv), LinearW4A16(self.o)
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.rope, self.interleaved = rope, interleaved
-        self._ws = None
+        self._ws, self._kept = None, []
 
     def workspace(self, batch: int, max_q: int, max_len: int, device) -> torch.Tensor:
         need = mq_kv_attention_workspace_bytes(batch, self.q_heads, self.kv_heads, self.head_dim, max_q, max_len)
         if self._ws is None or self._ws.numel() < need:
+            self._kept.append(self._ws)              # a captured graph may hold its address
             self._ws = workspace(need, device)
         return self._ws
 

@@ -274,3 +274,59 @@ def test_debug_build_checks_pass_and_match_the_release_build(tmp_path):
     assert int(got["hits"][0]) == 0
     for i, r in enumerate(release):
         assert np.array_equal(got[f"arr_{i}"], r), i
+
+
+# -- few rows (a slot per row), odd lengths -----------------------------------------------
+
+@pytest.mark.parametrize("seqs", [[(2, 17)], [(2, 1)], [(3, 2), (1, 1)], [(2, 0)], [(1, 16), (2, 33), (0, 3)], [(4, 18), (1, 32)]])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("q_heads,kv_heads", [(3, 3), (8, 1)])
+def test_a_few_rows(seqs, page, q_heads, kv_heads):
+    """Rows that cross a page, rows of padding in front, next to one another: the append bit for bit, the attention
+    of its Q over what it stored."""
+    bt = kv.Batch(seqs, page, kv_heads, 64, seed=len(seqs), extra_rows=1).fill()
+    table = kv.rope(64, 32)
+    qkv = torch.randn(bt.T, (q_heads + 2 * kv_heads) * 64, generator=torch.Generator().manual_seed(7)).bfloat16()
+    d = bt.to(dev())
+    q = torch.full((bt.T, q_heads, 64), -7.0, dtype=torch.bfloat16, device=dev())
+    ws = mq.workspace(mq.mq_kv_attention_workspace_bytes(len(seqs), q_heads, kv_heads, 64, bt.max_q, bt.max_len), dev())
+    mq.mq_rope_kv_append(qkv.to(dev()), table.to(dev()), q_out=q, ws=ws, interleaved=True, **d)
+    ref = kv.append_plain(bt, qkv, table, q_heads, 32, True, torch.float32)
+    mine = ~torch.isnan(ref)
+    assert torch.equal(q.cpu()[mine], ref.bfloat16()[mine]) and (q.cpu()[~mine] == -7.0).all()
+    assert torch.equal(d["k_codes"].view(torch.uint8).cpu(), bt.k) and torch.equal(d["v_codes"].view(torch.uint8).cpu(), bt.v)
+    assert torch.equal(d["k_scales"].cpu(), bt.ks)
+    out = torch.full_like(q, -7.0)
+    mq.mq_kv_attention(q, out=out, ws=ws, max_q=bt.max_q, max_len=bt.max_len, scale=0.125, **d)
+    assert mq.mq_read_status(ws) == mq.MQ_OK
+    want, bound = kv.attention_plain(bt, q.cpu(), 0.125)
+    nobody = torch.isnan(want)
+    assert (out.cpu()[nobody] == -7.0).all()
+    kv.close_to(out.cpu()[~nobody], want[~nobody], bound[~nobody])
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_lengths_below_zero(new):
+    """A length below zero is one of zero: nothing is appended, the rows see nothing."""
+    bt = kv.Batch([(new, 5), (new, 40)], 16, 1, 64, seed=9).fill()
+    d = bt.to(dev())
+    d["lens"][0] = -2 ** 31
+    before = d["k_codes"].view(torch.uint8).clone()
+    qkv = torch.randn(bt.T, 4 * 64, generator=torch.Generator().manual_seed(8)).bfloat16().to(dev())
+    q = torch.zeros(bt.T, 2, 64, dtype=torch.bfloat16, device=dev())
+    mq.mq_rope_kv_append(qkv, None, q_out=q, **d)
+    own = bt.table[1, :3].long()
+    others = [p for p in range(bt.pages) if p not in own.tolist()]
+    assert torch.equal(d["k_codes"].view(torch.uint8)[others], before[others])
+    out = torch.full_like(q, -7.0)
+    ws = mq.workspace(mq.mq_kv_attention_workspace_bytes(2, 2, 1, 64, new, 40), dev())
+    mq.mq_kv_attention(q, out=out, ws=ws, max_q=new, max_len=40, scale=0.125, **d)
+    assert mq.mq_read_status(ws) == mq.MQ_OK
+    assert (out[:new] == 0).all() and (out[new:] != -7.0).any()
+
+
+def test_a_workspace_that_grows_keeps_the_old_one():
+    block = _block(5)
+    a = block.workspace(1, 1, 100, dev())
+    b = block.workspace(8, 1, 100000, dev())
+    assert b.numel() > a.numel() and any(w is a for w in block._kept)
