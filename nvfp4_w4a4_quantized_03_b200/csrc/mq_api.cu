@@ -8,6 +8,7 @@
 
 #include "../../include/mq.h"
 #include "mq_internal.h"
+#include "mq_kv_internal.h"
 #include "mq_kv_plan.h"
 
 namespace {

@@ -5,8 +5,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "../../include/mq.h"
-
 namespace mq {
 
 // Workspace header, in 32-bit words.  Every kernel that uses it leaves the
@@ -88,48 +86,11 @@ struct GemmArgs {
     uint32_t* h_amax = nullptr;
 };
 
-// mq_rope_kv_append and mq_kv_attention (checked arguments of include/mq.h).
-struct KvAppendArgs {
-    const void* qkv;
-    int64_t T, row_stride;
-    int q_heads, rot_dim, interleaved;
-    const float* rope;
-    int64_t max_pos;
-    const mq_kv_cache* cache;
-    const mq_kv_batch* batch;
-    void* q_out;
-    int* status;             // may be null
-};
-cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
-
-struct KvAttentionArgs {
-    const void* q;
-    int64_t T, q_row_stride;
-    int q_heads;
-    const mq_kv_cache* cache;
-    const mq_kv_batch* batch;
-    int64_t max_q, max_len;
-    float scale;
-    void* out;
-    void* ws;
-};
-cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
-struct KvAttendParams;
-cudaError_t launch_kv_prefill(const KvAttendParams& p, int head_dim, int64_t blocks, cudaStream_t stream);
-
-// mq_linear_w4a16: M <= 64 rows of bf16 X against an NVFP4 weight.
-cudaError_t launch_linear_w4a16(const void* x, int64_t M, int64_t K, const uint8_t* w_codes, const uint8_t* w_scales,
-                                const float* alpha_w, int64_t N, void* y, int num_sms, cudaStream_t stream);
-
 // Debug build (MQ_DEBUG): bounds-check hits of each translation unit since
 // its last read (0 in the release build).
 unsigned long long debug_hits_quant();
 namespace gemm { unsigned long long debug_hits_gemm(); }
 namespace decode { unsigned long long debug_hits_decode(); }
-namespace kv_append { unsigned long long debug_hits_kv_append(); }
-namespace kv_attend { unsigned long long debug_hits_kv_attend(); }
-namespace kv_prefill { unsigned long long debug_hits_kv_prefill(); }
-namespace w4a16 { unsigned long long debug_hits_w4a16(); }
 
 // Readiness flags of the fused linear: one int per (128-row block, K stage).
 int64_t fused_flag_count(int64_t M, int64_t K);

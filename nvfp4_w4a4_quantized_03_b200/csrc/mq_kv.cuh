@@ -49,6 +49,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Of each half of a pair: the larger of a and |b|; a NaN in b counts as nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 struct KvAttendParams {
     const __nv_bfloat16* q;              // [T, q_stride]
     const int* cu;

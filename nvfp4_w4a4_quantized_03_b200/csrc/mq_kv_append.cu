@@ -25,10 +25,9 @@
 
 #include <algorithm>
 
-#include "../../include/mq.h"
 #include "mq_debug.cuh"
-#include "mq_internal.h"
 #include "mq_kv.cuh"
+#include "mq_kv_internal.h"
 #include "mq_ptx.cuh"
 
 namespace mq {

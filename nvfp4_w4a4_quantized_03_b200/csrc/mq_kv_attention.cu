@@ -29,10 +29,9 @@
 #include <cuda_fp16.h>
 
 
-#include "../../include/mq.h"
 #include "mq_debug.cuh"
-#include "mq_internal.h"
 #include "mq_kv.cuh"
+#include "mq_kv_internal.h"
 #include "mq_kv_plan.h"
 #include "mq_ptx.cuh"
 

@@ -38,10 +38,9 @@
 
 #include <type_traits>
 
-#include "../../include/mq.h"
 #include "mq_debug.cuh"
-#include "mq_internal.h"
 #include "mq_kv.cuh"
+#include "mq_kv_internal.h"
 #include "mq_kv_plan.h"
 #include "mq_ptx.cuh"
 

@@ -28,9 +28,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "../../include/mq.h"
 #include "mq_debug.cuh"
-#include "mq_internal.h"
+#include "mq_kv_internal.h"
 #include "mq_kv.cuh"
 #include "mq_ptx.cuh"
 
