@@ -497,17 +497,24 @@ class AttentionW4A4:
                  precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [T, hidden]: the new tokens of the batch (mq_kv_batch of mq.h);
         no sequence has more than max_q of them, or more than max_len tokens.
-        Rows that no sequence owns come out undefined."""
+        Rows that no sequence owns come out undefined.  On another stream than
+        the current one the call is what it is under torch.cuda.stream(stream):
+        its intermediate tensors, workspaces and output belong to that stream."""
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+            with torch.cuda.stream(stream):
+                return self(x, cache, cu_rows, lens, page_table, max_q, max_len, precise, out)
         T = x.shape[0]
         ws = self.workspace(page_table.shape[0], max_q, max_len, x.device)
-        qkv = (self.qkv_precise if precise else self.qkv)(x, stream=stream)
+        qkv = (self.qkv_precise if precise else self.qkv)(x)
         q = torch.empty(T, self.q_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
         attended = torch.empty_like(q)
         mq_rope_kv_append(qkv, self.rope, cu_rows, lens, page_table, *cache.tensors(), q, ws,
-                          interleaved=self.interleaved, stream=stream)
+                          interleaved=self.interleaved)
         mq_kv_attention(q, cu_rows, lens, page_table, *cache.tensors(), attended, ws, max_q, max_len,
-                        self.head_dim ** -0.5, stream)
-        return (self.o_precise if precise else self.o)(attended.view(T, -1), out, stream)
+                        self.head_dim ** -0.5)
+        return (self.o_precise if precise else self.o)(attended.view(T, -1), out)
 
     def status(self, stream=None) -> int:
         """The workspace's status word (mq_read_status): MQ_ERR_INVALID_ARG when

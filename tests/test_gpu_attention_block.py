@@ -330,3 +330,25 @@ def test_a_workspace_that_grows_keeps_the_old_one():
     a = block.workspace(1, 1, 100, dev())
     b = block.workspace(8, 1, 100000, dev())
     assert b.numel() > a.numel() and any(w is a for w in block._kept)
+
+
+@pytest.mark.parametrize("as_address", [False, True])
+def test_block_on_another_stream_than_the_current_one(as_address):
+    """The block's intermediate tensors are that stream's: what the current stream allocates meanwhile is elsewhere."""
+    block = _block(6)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(4, HID, generator=g).bfloat16().to(dev())
+    table = torch.arange(4, dtype=torch.int32, device=dev())[:, None].contiguous()
+    lens, cu = _i32(1, 1, 1, 1), _i32(0, 1, 2, 3, 4)
+    caches = [mq.PagedKVCache(4, P, HKV, D, dev()) for _ in range(2)]
+    want = block(x, caches[0], cu, lens, table, 1, P, precise=True)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                                    # about 10 ms: the calls below stand behind it
+    got = block(x, caches[1], cu, lens, table, 1, P, precise=True, stream=s.cuda_stream if as_address else s)
+    sizes = [(4, (HQ + 2 * HKV) * D), (4, HQ, D), (4, HQ, D), (4, HID)]
+    others = [torch.full(size, 7.0, dtype=torch.bfloat16, device=dev()) for size in sizes * 4]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all((t == 7.0).all() for t in others)
