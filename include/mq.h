@@ -289,7 +289,7 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  * and statistics in binary32, the output rounded once to bf16.
  *   q       : device bf16 [T, q_row_stride], a row's heads at its front;
  *             q_row_stride >= q_heads head_dim, a multiple of 8
- *   out     : device bf16 [T, q_heads, head_dim], written
+ *   out     : device bf16 [T, q_heads, head_dim], written; it may not overlap q
  *   q_heads : a multiple of kv_heads, at most 128 times as many
  *   max_q, max_len : no sequence has more new tokens, or a greater length
  *             (host values, e.g. fixed for a captured graph; one that has

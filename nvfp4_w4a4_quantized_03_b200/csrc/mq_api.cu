@@ -436,10 +436,12 @@ int mq_rope_kv_append(const void* qkv, int64_t T, int64_t row_stride, int32_t q_
 
 static bool kv_attention_sizes_ok(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t max_q,
                                   int64_t max_len) {
-    return batch >= 1 && batch <= 1 << 20 && kv_heads >= 1 && kv_heads <= 1024 && q_heads >= kv_heads &&
-           q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 && (head_dim == 64 || head_dim == 128) &&
-           max_q >= 1 && max_q <= 1 << 24 && max_q * (q_heads / kv_heads) <= 0x7fff0000 && max_len >= 0 &&
-           max_len <= 0x7fff0000;
+    if (batch < 1 || batch > 1 << 20 || kv_heads < 1 || kv_heads > 1024 || q_heads < kv_heads ||
+        q_heads % kv_heads != 0 || q_heads / kv_heads > 128 || (head_dim != 64 && head_dim != 128) || max_q < 1 ||
+        max_q > 1 << 24 || max_q * (q_heads / kv_heads) > 0x7fff0000 || max_len < 0 || max_len > 0x7fff0000)
+        return false;
+    const mq::KvPlan plan = mq::kv_plan(batch, q_heads, kv_heads, head_dim, max_q, max_len);
+    return plan.cells * plan.chunks <= 0x7fffffff;                    // blocks of the launch
 }
 
 size_t mq_kv_attention_workspace_bytes(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -461,7 +463,6 @@ int mq_kv_attention(const void* q, int64_t T, int64_t q_row_stride, int32_t q_he
     if (!(scale > 0.f) || scale > 3.0e38f) return MQ_ERR_INVALID_ARG;
     const mq::KvPlan plan =
         mq::kv_plan(batch->batch, q_heads, cache->kv_heads, cache->head_dim, max_q, max_len);
-    if (plan.cells * plan.chunks > 0x7fffffff) return MQ_ERR_SHAPE;
     if (!ws || ws_bytes < (size_t)plan.bytes) return MQ_ERR_WORKSPACE;
     if (!aligned16(q) || !aligned16(out) || !aligned256(ws)) return MQ_ERR_ALIGN;
     int sms = 0;

@@ -109,6 +109,13 @@ def test_attention_workspace(L):
     assert f(1, 8, 8, 128, 1, 1 << 30) <= one + 8 * 128 * 8 * 130 * 4
 
 
+def test_attention_workspace_of_more_blocks_than_a_launch_has(L):
+    """batch x row tiles x kv heads of 2^31 is refused, and has no workspace size."""
+    f = mq.mq_kv_attention_workspace_bytes
+    assert f(1 << 20, 1024, 1024, 128, 16, 8) > 0                   # one row tile of 16: 2^30 blocks
+    assert f(1 << 20, 1024, 1024, 128, 257, 8) == 0                 # two of 256
+
+
 @pytest.mark.parametrize("want,M,N,K,kw", [
     (SHAPE, 0, 64, 64, {}), (SHAPE, 65, 64, 64, {}), (SHAPE, 1, 64, 96, {}), (SHAPE, 1, 0, 64, {}),
     (INVALID, 1, 64, 64, dict(x=None)), (INVALID, 1, 64, 64, dict(alpha=None)), (ALIGN, 1, 64, 64, dict(x=ctypes.c_void_p(4104))),
