@@ -72,6 +72,7 @@ struct KvAttendParams {
     int64_t T, q_stride, num_pages, max_pages, max_len;
     int batch, q_heads, kv_heads, group, page_log2, max_q;
     int row_tiles, chunks, chunk_tokens;
+    int by_length;                       // tcgen05 form: blocks in the order of the keys they see
     float scale_log2;
 };
 

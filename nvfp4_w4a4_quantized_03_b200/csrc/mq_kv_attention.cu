@@ -434,6 +434,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {
     p.row_tiles = (int)plan.row_tiles;
     p.chunks = (int)plan.chunks;
     p.chunk_tokens = (int)plan.chunk_tokens;
+    p.by_length = plan.by_length;
     p.scale_log2 = a.scale * 1.44269504088896340736f;
     const int64_t blocks = plan.cells * plan.chunks;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;

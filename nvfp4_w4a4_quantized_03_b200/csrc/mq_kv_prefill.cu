@@ -67,6 +67,7 @@ struct Smem {
     uint32_t tmem_base;
     int abort_flag;
     int last;
+    int seq, tile;                              // by_length
 };
 
 template <int D>
@@ -159,6 +160,81 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
     asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
+// The row tiles of the whole batch in the order of the keys they see (in units
+// of 64), most first, so that the last blocks to start are short ones: warp 0
+// finds tile `job` of that order.  A sequence's tiles from tmin(v) on see 64 v
+// keys or more; a search over v with a sum over the batch gives the v of tile
+// `job`.  N: sequences per lane.
+template <int N>
+__device__ __forceinline__ void by_length(const KvAttendParams& p, int job, Smem* s) {
+    const int lane = threadIdx.x % 32;
+    int start[N], len[N], own[N], longest = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int b = lane + 32 * i;
+        start[i] = len[i] = own[i] = 0;
+        if (b < p.batch) {
+            const int64_t c0 = p.cu[b], n = p.cu[b + 1] - c0;
+            const int l = max(p.lens[b], 0);
+            if (n <= 0) continue;
+            own[i] = 1;                                      // of a sequence that is refused: the block that reports it
+            if (c0 < 0 || c0 + n > p.T || n > p.max_q || l > p.max_len || l > p.max_pages << p.page_log2) continue;
+            own[i] = (int)((n * p.group + ROWS - 1) / ROWS);
+            start[i] = l - (int)n;
+            len[i] = l;
+            longest = max(longest, l);
+        }
+    }
+    if (lane == 0) s->seq = -1;
+    __syncwarp();
+    // sequences alike need no search
+    const int own0 = __shfl_sync(0xffffffffu, own[0], 0), len0 = __shfl_sync(0xffffffffu, len[0], 0);
+    bool alike = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) alike = alike && (lane + 32 * i >= p.batch || (own[i] == own0 && len[i] == len0));
+    if (__all_sync(0xffffffffu, alike)) {
+        if (lane == 0 && job / p.batch < own0) {
+            s->seq = job % p.batch;
+            s->tile = own0 - 1 - job / p.batch;
+        }
+        return;
+    }
+    auto tmin = [&](int i, int v) {
+        return v <= 0 ? 0 : v > len[i] >> 6 ? own[i] : max(0, (v << 6) - 1 - start[i]) * p.group / ROWS;
+    };
+    auto count = [&](int v) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += own[i] - tmin(i, v);
+        return __reduce_add_sync(0xffffffffu, sum);
+    };
+    int lo = 0, hi = (__reduce_max_sync(0xffffffffu, longest) >> 6) + 1;
+    if (count(0) <= job) return;                             // no such tile
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (count(mid) > job)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    int left = job - count(hi);                              // among the tiles that see 64 lo .. 64 lo + 63 keys
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int first = tmin(i, lo), mine = tmin(i, hi) - first;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (left >= upto - mine && left < upto) {
+            s->seq = lane + 32 * i;
+            s->tile = first + left - (upto - mine);
+        }
+        left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     using L = Layout<D>;
@@ -170,13 +246,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
     pdl_launch_dependents();
     pdl_wait();
 
-    // chunk fastest, then kv head, sequence; the last row tiles (they see most) first
+    // chunk fastest, then kv head, sequence; the last row tiles (they see most)
+    // first, those of a ragged batch by what they see
     int id = blockIdx.x;
     const int chunk = id % p.chunks;
     id /= p.chunks;
     const int head = id % p.kv_heads;
     id /= p.kv_heads;
-    const int b = id % p.batch, tile = p.row_tiles - 1 - id / p.batch;
+    int b = id % p.batch, tile = p.row_tiles - 1 - id / p.batch;
+    if (p.by_length) {
+        if (warp == 0) {
+            if (p.batch <= 32)
+                by_length<1>(p, id, s);
+            else
+                by_length<KV_BY_LENGTH_MAX / 32>(p, id, s);
+        }
+        __syncthreads();
+        b = s->seq;
+        tile = s->tile;
+        if (b < 0) return;
+    }
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
     const int64_t len = max(p.lens[b], 0);
     const int page_tokens = 1 << p.page_log2;

@@ -244,6 +244,39 @@ def test_attention_lengths_beyond_the_call_are_reported():
         kv.close_to(out[good], want[good], bound[good])
 
 
+# Batches of more tiles than run at once: their blocks take the sequences in the order of the keys they see.
+WAVES = {
+    "ragged": [(600, 900), (37, 2000), (0, 50), (1, 1), (599, 599), (130, 1200), (33, 2), (600, 601)],
+    "alike": [(300, 300)] * 8,
+    "more than a warp": [(3 + 11 * i % 40, 5 + 37 * i % 300) for i in range(40)],
+    "as many as are ordered": [(i % 7, (17 * i) % 90) for i in range(127)] + [(40, 90)],
+    "more than are ordered": [(i % 4, (17 * i) % 90) for i in range(130)],
+}
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("seqs", list(WAVES))
+def test_attention_more_tiles_than_run_at_once(seqs, head_dim):
+    bt = kv.Batch(WAVES[seqs], 16, 2, head_dim, seed=40, extra_rows=2).fill()
+    _check_attention(bt, 16, seed=3, max_q=max(600, bt.max_q))
+
+
+def test_attention_more_tiles_than_run_at_once_lengths_beyond_the_call():
+    """Sequences that the call refuses among others: reported, left alone, the others computed."""
+    bt = kv.Batch([(600, 700), (20, 1000), (70, 80), (5, 2000), (601, 601), (1, 700)], 16, 2, 64, seed=41).fill()
+    q = torch.randn(bt.T, 16, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    want, bound = kv.attention_plain(bt, q, 0.125)
+    ws = mq.workspace(mq.mq_kv_attention_workspace_bytes(6, 16, 2, 64, 600, 1000), dev())
+    out = torch.full(q.shape, -7.0, dtype=torch.bfloat16, device=dev())
+    mq.mq_kv_attention(q.to(dev()), out=out, ws=ws, max_q=600, max_len=1000, scale=0.125, **bt.to(dev()))
+    assert mq.mq_read_status(ws) == -1
+    bad = torch.zeros(bt.T, dtype=torch.bool)
+    bad[690:695] = bad[695:1296] = True                                   # the fourth (length) and the fifth (rows)
+    out = out.cpu()
+    assert (out[bad] == -7.0).all()
+    kv.close_to(out[~bad], want[~bad], bound[~bad])
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_page_numbers_outside_the_pool_are_reported(new):
     bt = kv.Batch([(new, 60), (new, 60)], 16, 1, 64, seed=36).fill()
