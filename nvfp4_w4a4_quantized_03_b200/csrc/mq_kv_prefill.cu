@@ -135,7 +135,8 @@ __device__ __forceinline__ float ex2v(float x) {
 // (it appears in the low bits of x + 1.5 * 2^23), 2^f = 1 + f (c1 + f (c2 + f (c3 + f c4)))
 // with coefficients fitted here to the least largest relative error on
 // [-1/2, 1/2], 2^-18.4; i goes into the exponent.  Below 2^-126 the result
-// runs out towards 0, which it is from -127 on (-inf too).
+// runs out towards 0, which it is from -127 on (-inf too).  Of a NaN it makes a
+// number: the row's sum has it from the maximum.
 __device__ __forceinline__ void exp2_pair(float& x, float& y) {
     const uint64_t v = pack2(fmaxf(x, -127.f), fmaxf(y, -127.f));
     const uint64_t t = add2(v, pack2(12582912.f, 12582912.f));
@@ -150,9 +151,15 @@ __device__ __forceinline__ void exp2_pair(float& x, float& y) {
     x = __uint_as_float(__float_as_uint(c) + (__float_as_uint(a) << 23));
     y = __uint_as_float(__float_as_uint(d) + (__float_as_uint(b) << 23));
 }
+// the larger, a NaN before all others
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
     return r;
 }
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
@@ -433,11 +440,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
                                 g0 = max3(__float_as_uint(g0), x[i], x[i + 1]);
                                 g1 = max3(__float_as_uint(g1), x[i + 2], x[i + 3]);
                             }
-                            g0 = fmaxf(max3(__float_as_uint(g0), x[14], x[15]), g1);
-                            top = fmaxf(top, __fmaf_rn(g0, fck[2 * c + g], sh[2 * c + g]));
+                            g0 = max2(max3(__float_as_uint(g0), x[14], x[15]), g1);
+                            top = max2(top, __fmaf_rn(g0, fck[2 * c + g], sh[2 * c + g]));
                         }
                     }
                 }
+                // A NaN among the scores the row sees, or an infinite one, is
+                // a NaN in its sum from here on, and so in its output:
+                // exp2_pair would make a number of it.
+                if (!(top < INFINITY)) l = NAN;
                 if (__any_sync(0xffffffffu, top > m + LAZY)) {
                     const float f = top > m + LAZY ? ex2(m - top) : 1.f;
                     if (top > m + LAZY) m = top;
