@@ -283,7 +283,9 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  *
  * mq_kv_attention: for the new token of row r at position p of its sequence, head h
  *   out[r, h] = sum_j softmax_j(scale q[r, h] . k[j]) v[j], j = 0 .. min(p, lens[b] - 1),
- * k, v of kv head h / (q_heads / kv_heads); zero where there is no j.
+ * k, v of kv head h / (q_heads / kv_heads); zero where there is no j.  Keys of
+ * a page whose number is outside the pool are left out, as if there were no
+ * such j, and the workspace's status word takes MQ_ERR_INVALID_ARG.
  * Products are of f16 operands (the cache's codes are exact in f16, q goes to
  * f16 under a power of two per row, the softmax weights round to f16), sums
  * and statistics in binary32, the output rounded once to bf16.

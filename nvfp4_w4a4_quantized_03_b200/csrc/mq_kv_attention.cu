@@ -204,11 +204,13 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? (D == 64 ? 5 : 4) : (D == 6
         for (int i = 0; i < 4; ++i)
             if (MQ_CHECK(base + (2 * t + (i & 1) + 8 * (i >> 1)) * D + (g + 1) * (VW * 4) <= pool))
                 load_codes(vw[i], src + ((i & 1) + 8 * (i >> 1)) * D);
-        if (tok0 + STEP > k1) {
-            // behind the last token a page holds whatever was there: a NaN code times a zero weight is no zero
+        if (tok0 + STEP > k1 || !valid) {
+            // behind the last token a page holds whatever was there, and so does
+            // the pool's first page in place of one that is none: a NaN code
+            // times a zero weight is no zero
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (tok0 + 2 * t + (i & 1) + 8 * (i >> 1) >= k1) {
+                if (tok0 + 2 * t + (i & 1) + 8 * (i >> 1) >= k1 || !valid) {
 #pragma unroll
                     for (int w = 0; w < VW; ++w) vw[i][w] = 0;
                 }

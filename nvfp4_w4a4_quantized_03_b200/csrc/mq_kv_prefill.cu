@@ -62,13 +62,18 @@ constexpr long long TIMEOUT_CYCLES = 4000000000LL;
 struct Smem {
     uint64_t q_full, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t s_full[2], p_full[2], o_full[2], t_full[TABLES], t_empty[TABLES], drained;
-    int64_t off[TABLES][GROUPS];                // byte offset of a group's codes in the pool, -1: none
+    const uint8_t* k_at[TABLES][GROUPS];        // a group's codes in the pool; g_zeros where it has no page
+    const uint8_t* v_at[TABLES][GROUPS];
     float ck[TABLES][GROUPS], ev[TABLES][GROUPS], iev[TABLES][GROUPS];
     uint32_t tmem_base;
     int abort_flag;
     int last;
     int seq, tile;                              // by_length
 };
+
+// What a group without a page is read from: zeros (what the pool holds in its
+// place may be a NaN code, which times a zero weight is no zero).
+__device__ uint4 g_zeros[16 * 128 / 16];
 
 template <int D>
 struct Layout {
@@ -546,13 +551,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         const int within = (tok & 15) * D + piece * 16;
         [[maybe_unused]] const int64_t pool = (p.num_pages * p.kv_heads << p.page_log2) * D;
         uint4 kc[PASSES], vc[PASSES];
-        auto load = [&](uint4 (&c)[PASSES], const uint8_t* codes, int j) {
-            const int64_t* off = s->off[j % TABLES];
+        auto load = [&](uint4 (&c)[PASSES], const uint8_t* const (&groups)[TABLES][GROUPS],
+                        [[maybe_unused]] const uint8_t* codes, int j) {
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
-                const int64_t o = max(off[q * TOKENS / 16 + (TOKENS == 32 ? tok >> 4 : 0)], (int64_t)0) + within;
+                const uint8_t* at = groups[j % TABLES][q * TOKENS / 16 + (TOKENS == 32 ? tok >> 4 : 0)] + within;
                 c[q] = make_uint4(0, 0, 0, 0);
-                if (MQ_CHECK(o + 16 <= pool)) c[q] = load_codes(codes + o);
+                if (MQ_CHECK(at - within == reinterpret_cast<const uint8_t*>(g_zeros) || (at >= codes && at + 16 <= codes + pool)))
+                    c[q] = load_codes(at);
             }
             // behind the last key a page holds whatever was there, a NaN code
             // times a zero weight is no zero: zeros instead
@@ -581,8 +587,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
         };
         bool ok = wait(&s->t_full[0], 0);
         if (ok) {
-            load(kc, p.k_codes, 0);
-            load(vc, p.v_codes, 0);
+            load(kc, s->k_at, p.k_codes, 0);
+            load(vc, s->v_at, p.v_codes, 0);
             if (lane == 0) mbar_arrive(&s->t_empty[0]);
         }
         for (int j = 0; ok && j < blocks; ++j) {
@@ -596,33 +602,33 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
             if (more) {
                 ok = wait(&s->t_full[nt], ((j + 1) / TABLES) & 1);
                 if (!ok) break;
-                load(kc, p.k_codes, j + 1);
+                load(kc, s->k_at, p.k_codes, j + 1);
             }
             ok = wait(&s->v_empty[st], phase ^ 1);
             if (!ok) break;
             store(sbase + L::V_OFF + st * L::TILE_BYTES, vc);
             if (lane == 0) mbar_arrive(&s->v_full[st]);
             if (more) {
-                load(vc, p.v_codes, j + 1);
+                load(vc, s->v_at, p.v_codes, j + 1);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s->t_empty[nt]);
             }
         }
     } else if (warp == TABLE_WARP) {
         // ------------------------------------------------------------ tables
-        // of the blocks to come: lane g looks up group g
+        // of the blocks to come: lane g looks up K's side of group g, lane g + 8 V's
         for (int j = 0; j < blocks; ++j) {
             const int tb = j % TABLES;
             int64_t off = -1;
-            float gk = 0.f, gv = 1.f;
-            const int at = k0 + j * BLOCK + lane * 16;
-            if (lane < GROUPS && at < k1) {
+            const uint8_t* zeros = reinterpret_cast<const uint8_t*>(g_zeros);
+            float scale = 1.f;
+            const int g = lane % GROUPS, at = k0 + j * BLOCK + g * 16;
+            if (lane < 2 * GROUPS && at < k1) {
                 const int64_t page = p.table[(int64_t)b * p.max_pages + (at >> p.page_log2)];
                 if (page >= 0 && page < p.num_pages) {
                     const int64_t cell = page * p.kv_heads + head;
                     off = ((cell << p.page_log2) + (at & (page_tokens - 1))) * D;
-                    gk = p.k_scales[cell];
-                    gv = p.v_scales[cell];
+                    scale = (lane < GROUPS ? p.k_scales : p.v_scales)[cell];
                 } else if (p.status) {
                     atomicExch(p.status, MQ_ERR_INVALID_ARG);
                 }
@@ -630,10 +636,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(KvAttendParams p) {
             __syncwarp();
             if (!wait(&s->t_empty[tb], ((j / TABLES) & 1) ^ 1)) break;
             if (lane < GROUPS) {
-                s->off[tb][lane] = off;
-                s->ck[tb][lane] = gk;
-                s->ev[tb][lane] = (float)((int)(__float_as_uint(gv) >> 23) - 127);
-                s->iev[tb][lane] = __uint_as_float((254u << 23) - (__float_as_uint(gv) & 0x7F800000u));
+                s->k_at[tb][g] = off < 0 ? zeros : p.k_codes + off;
+                s->ck[tb][g] = off < 0 ? 0.f : scale;
+            } else if (lane < 2 * GROUPS) {
+                s->v_at[tb][g] = off < 0 ? zeros : p.v_codes + off;
+                s->ev[tb][g] = off < 0 ? -INFINITY : (float)((int)(__float_as_uint(scale) >> 23) - 127);
+                s->iev[tb][g] = __uint_as_float((254u << 23) - (__float_as_uint(scale) & 0x7F800000u));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s->t_full[tb]);

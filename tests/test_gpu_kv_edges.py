@@ -1,6 +1,6 @@
 """Edges of the attention over the paged E4M3 cache (mq_kv_attention), in the
 form for few rows and in the tcgen05 form: a NaN at every place of a group of 16
-keys.  Plain forms and bounds as in test_gpu_kv."""
+keys, page numbers outside the pool.  Plain forms and bounds as in test_gpu_kv."""
 import pytest
 import torch
 
@@ -48,3 +48,30 @@ def test_a_nan_at_every_place_of_a_group(new, length, first, head_dim, where):
     assert torch.isnan(got[sees]).all()
     want, bound = (t.view(16, new, 2, head_dim) for t in kv.attention_plain(last, q, 0.125))
     kv.close_to(got[~sees], want[~sees], bound[~sees])
+
+
+@pytest.mark.parametrize("number", ["behind", "negative"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("new,length", [(1, 70), (4, 70), (30, 70), (30, 2100)])
+def test_keys_of_a_page_outside_the_pool_are_left_out(new, length, head_dim, number):
+    """As if the sequence did not hold them; a sequence without any valid page sees nothing.  The status word says so."""
+    bad, page = 1, 16
+    bt = kv.Batch([(new, length), (new, length), (new, length)], page, 2, head_dim, seed=length, extra_pages=3).fill()
+    # the pool's first page is nobody's, NaN all over
+    bt.table[bt.table >= 0] += 1
+    bt.pages += 1
+    bt.k, bt.v = (torch.cat([torch.full_like(t[:1], 0x7F), t]) for t in (bt.k, bt.v))
+    bt.ks, bt.vs = (torch.cat([t[:1], t]) for t in (bt.ks, bt.vs))
+    q = _q(bt, 8, 1)
+    # the same without the page: all rows stand behind it
+    short = kv.Batch([(new, length - page)] * 3, page, 2, head_dim, extra_pages=0)
+    short.table = torch.cat([bt.table[:, :bad], bt.table[:, bad + 1:]], 1)
+    short.pages, short.k, short.v, short.ks, short.vs = bt.pages, bt.k, bt.v, bt.ks, bt.vs
+    want, bound = kv.attention_plain(bt, q, 0.125)
+    want[:new], bound[:new] = (t[:new] for t in kv.attention_plain(short, q, 0.125))
+    want[new:2 * new] = bound[new:2 * new] = 0
+    d = bt.to(dev())
+    d["page_table"][0, bad] = d["page_table"][1, :] = bt.pages if number == "behind" else -2
+    got = _attend(bt, d, q, 0.125, status=-1)
+    assert (got[new:2 * new] == 0).all()
+    kv.close_to(got, want, bound)
