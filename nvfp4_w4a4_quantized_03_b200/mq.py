@@ -497,7 +497,10 @@ class AttentionW4A4:
                  precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [T, hidden]: the new tokens of the batch (mq_kv_batch of mq.h);
         no sequence has more than max_q of them, or more than max_len tokens.
-        Rows that no sequence owns come out undefined.  On another stream than
+        Rows that no sequence owns, and those of a sequence that has more, come
+        out undefined (zero from the quantizing linears) and leave the others
+        as they are, but for one thing: the QKV linear's tensor scale is taken
+        over all rows of x, so padding rows should be zeros.  On another stream than
         the current one the call is what it is under torch.cuda.stream(stream):
         its intermediate tensors, workspaces and output belong to that stream."""
         if stream is not None:
@@ -507,9 +510,11 @@ class AttentionW4A4:
                 return self(x, cache, cu_rows, lens, page_table, max_q, max_len, precise, out)
         T = x.shape[0]
         ws = self.workspace(page_table.shape[0], max_q, max_len, x.device)
-        qkv = (self.qkv_precise if precise else self.qkv)(x)
         q = torch.empty(T, self.q_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
-        attended = torch.empty_like(q)
+        # the quantizing O linear takes one tensor scale over all rows, those too
+        # that the attention does not write
+        attended = torch.empty_like(q) if precise else torch.zeros_like(q)
+        qkv = (self.qkv_precise if precise else self.qkv)(x)
         mq_rope_kv_append(qkv, self.rope, cu_rows, lens, page_table, *cache.tensors(), q, ws,
                           interleaved=self.interleaved)
         mq_kv_attention(q, cu_rows, lens, page_table, *cache.tensors(), attended, ws, max_q, max_len,

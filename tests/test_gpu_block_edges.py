@@ -1,0 +1,77 @@
+"""Edges of the attention block (AttentionW4A4): rows that no sequence owns or
+that belong to a refused one, beside the O linear's one tensor scale."""
+import pytest
+import torch
+
+from nvfp4_w4a4_quantized_03_b200 import inputs, mq
+from tests.gpu_helpers import dev
+
+pytestmark = pytest.mark.gpu
+HID, HQ, HKV, D, P = 512, 8, 2, 64, 16
+
+
+def _block(seed=0, positions=5000):
+    w_qkv = inputs.weight_bf16((HQ + 2 * HKV) * D, HID, seed=seed)
+    w_o = inputs.weight_bf16(HID, HQ * D, seed=seed + 1)
+    return mq.AttentionW4A4(w_qkv.to(dev()), w_o.to(dev()), HQ, HKV, D, mq.rope_table(positions, D, device=dev()))
+
+
+def _i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device=dev())
+
+
+def _x(T, seed=0):
+    return torch.randn(T, HID, generator=torch.Generator().manual_seed(seed)).bfloat16().to(dev())
+
+
+def _steps(block, x, cache, cu, lens, table, max_q, max_len, precise=False):
+    """The block's calls one by one; rows that the attention does not write are zero in the O linear's input."""
+    T = x.shape[0]
+    qkv = (block.qkv_precise if precise else block.qkv)(x)
+    q = torch.zeros(T, HQ, D, dtype=torch.bfloat16, device=dev())
+    out = torch.zeros_like(q)
+    ws = mq.workspace(mq.mq_kv_attention_workspace_bytes(table.shape[0], HQ, HKV, D, max_q, max_len), dev())
+    mq.mq_rope_kv_append(qkv, block.rope, cu, lens, table, *cache.tensors(), q)
+    mq.mq_kv_attention(q, cu, lens, table, *cache.tensors(), out, ws, max_q, max_len, D ** -0.5)
+    return (block.o_precise if precise else block.o)(out.view(T, -1))
+
+
+@pytest.fixture
+def poisoned(monkeypatch):
+    """Memory that torch hands out uninitialised holds `value`."""
+    def poison(value):
+        empty, empty_like = torch.empty, torch.empty_like
+
+        def fill(t):
+            return t.fill_(value) if t.is_floating_point() and t.is_cuda else t
+        monkeypatch.setattr(torch, "empty", lambda *a, **k: fill(empty(*a, **k)))
+        monkeypatch.setattr(torch, "empty_like", lambda *a, **k: fill(empty_like(*a, **k)))
+    return poison
+
+
+@pytest.mark.parametrize("value", [float("nan"), 1e30, float("inf")])
+def test_rows_of_nobody_leave_the_others_alone(poisoned, value):
+    """A batch of two prompts padded to more rows: the prompts' rows are those of the unpadded call."""
+    block, table = _block(), torch.arange(16, dtype=torch.int32, device=dev()).view(2, 8)
+    x = _x(150)
+    x[103:] = 0
+    args = (_i32(0, 70, 103), _i32(70, 33), table, 70, 128)
+    want = block(x[:103], mq.PagedKVCache(16, P, HKV, D, dev()), *args)
+    poisoned(value)
+    got = block(x, mq.PagedKVCache(16, P, HKV, D, dev()), *args)
+    assert block.status() == mq.MQ_OK
+    assert torch.equal(got[:103], want)
+    assert (got[103:] == 0).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), 1e30])
+def test_a_refused_sequence_leaves_the_others_alone(poisoned, value):
+    """One of three sequences is longer than max_len: reported, the others as step by step."""
+    block, table = _block(1), torch.arange(48, dtype=torch.int32, device=dev()).view(3, 16)
+    x = _x(120, 1)
+    args = (_i32(0, 50, 80, 120), _i32(50, 200, 60), table, 50, 128)
+    want = _steps(block, x, mq.PagedKVCache(48, P, HKV, D, dev()), *args)
+    poisoned(value)
+    got = block(x, mq.PagedKVCache(48, P, HKV, D, dev()), *args)
+    assert block.status() == -1
+    assert torch.equal(got, want) and torch.isfinite(got).all()
