@@ -496,7 +496,8 @@ class AttentionW4A4:
     def __call__(self, x: torch.Tensor, cache: PagedKVCache, cu_rows, lens, page_table, max_q: int, max_len: int,
                  precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x [T, hidden]: the new tokens of the batch (mq_kv_batch of mq.h);
-        no sequence has more than max_q of them, or more than max_len tokens.
+        no sequence has more than max_q of them, or more than max_len tokens, or
+        more than the rotary table has positions.
         Rows that no sequence owns, and those of a sequence that has more, come
         out undefined (zero from the quantizing linears) and leave the others
         as they are, but for one thing: the QKV linear's tensor scale is taken
@@ -509,6 +510,9 @@ class AttentionW4A4:
             with torch.cuda.stream(stream):
                 return self(x, cache, cu_rows, lens, page_table, max_q, max_len, precise, out)
         T = x.shape[0]
+        if self.rope is not None:
+            # the append leaves the rows of positions behind the table's: so does the attention
+            max_len = min(max_len, self.rope.shape[0])
         ws = self.workspace(page_table.shape[0], max_q, max_len, x.device)
         q = torch.empty(T, self.q_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
         # the quantizing O linear takes one tensor scale over all rows, those too

@@ -75,3 +75,17 @@ def test_a_refused_sequence_leaves_the_others_alone(poisoned, value):
     got = block(x, mq.PagedKVCache(48, P, HKV, D, dev()), *args)
     assert block.status() == -1
     assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), 1e30])
+def test_a_sequence_longer_than_the_rotary_table_leaves_the_others_alone(poisoned, value):
+    """The append leaves the rows of positions that the table does not have; the attention does not take up what
+    memory held in their place."""
+    block, table = _block(2, positions=64), torch.arange(48, dtype=torch.int32, device=dev()).view(3, 16)
+    x = _x(120, 2)
+    cu, lens = _i32(0, 50, 80, 120), _i32(50, 90, 60)
+    want = _steps(block, x, mq.PagedKVCache(48, P, HKV, D, dev()), cu, lens, table, 50, 64)
+    poisoned(value)
+    got = block(x, mq.PagedKVCache(48, P, HKV, D, dev()), cu, lens, table, 50, 200)
+    assert block.status() == -1
+    assert torch.equal(got, want) and torch.isfinite(got).all()
