@@ -95,6 +95,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """A stream or its address as torch's stream (address 0: the default one,
+    which ExternalStream would take for a new stream)."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
+
 def _check(status: int, what: str):
     if status != MQ_OK:
         raise MQError(status, what)
@@ -505,9 +513,7 @@ class AttentionW4A4:
         the current one the call is what it is under torch.cuda.stream(stream):
         its intermediate tensors, workspaces and output belong to that stream."""
         if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=x.device)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(_torch_stream(stream, x.device)):
                 return self(x, cache, cu_rows, lens, page_table, max_q, max_len, precise, out)
         T = x.shape[0]
         if self.rope is not None:

@@ -89,3 +89,18 @@ def test_a_sequence_longer_than_the_rotary_table_leaves_the_others_alone(poisone
     got = block(x, mq.PagedKVCache(48, P, HKV, D, dev()), cu, lens, table, 50, 200)
     assert block.status() == -1
     assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+def test_the_default_stream_by_its_address():
+    """stream=0 is the default stream, whatever the current one: the call stands behind what it holds."""
+    block, table, (old, new) = _block(3), _i32(0, 1)[None], (_x(1, 5), _x(1, 6))
+    args = (_i32(0, 1), _i32(1), table, 1, 32, True)
+    want = block(new, mq.PagedKVCache(2, P, HKV, D, dev()), *args)
+    x, cache, side = old.clone(), mq.PagedKVCache(2, P, HKV, D, dev()), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                                        # about 10 ms on the default stream
+    x.copy_(new)
+    with torch.cuda.stream(side):
+        got = block(x, cache, *args, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
