@@ -117,17 +117,24 @@ int32_t int32_of(int64_t v, const char* what) {
     return (int32_t)v;
 }
 
-// Runs f, with its refusals and torch's exceptions as Python errors; the status as an int.
+// Runs f, with its refusals and torch's exceptions as Python errors; false with one.
 template <typename F>
-PyObject* guarded(F f) {
+bool guarded_void(F f) {
     try {
-        return PyLong_FromLong(f());
+        f();
+        return true;
     } catch (const Refused& r) {
         PyErr_SetString(PyExc_ValueError, r.why.c_str());
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
-    return nullptr;
+    return false;
+}
+// The same; f's status as an int.
+template <typename F>
+PyObject* guarded(F f) {
+    int status = 0;
+    return guarded_void([&] { status = f(); }) ? PyLong_FromLong(status) : nullptr;
 }
 
 PyObject* py_bind(PyObject*, PyObject* args) {
@@ -227,11 +234,25 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// stream, device index (negative: the current device) -> (device index, the stream's address)
+PyObject* py_place(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    long long index;
+    if (!count(n, 2) || !number(args[1], &index)) return nullptr;
+    void* stream = nullptr;
+    if (!guarded_void([&] {
+            if (index < 0) index = c10::cuda::current_device();
+            stream = stream_of(args[0], (int)index);
+        }))
+        return nullptr;
+    return Py_BuildValue("(LK)", index, (unsigned long long)(uintptr_t)stream);
+}
+
 PyMethodDef g_methods[] = {
     {"bind", py_bind, METH_VARARGS, "addresses of mq_linear_w4a16, mq_rope_kv_append, mq_kv_attention"},
     {"linear", reinterpret_cast<PyCFunction>(py_linear), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(py_append), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(py_attention), METH_FASTCALL, nullptr},
+    {"place", reinterpret_cast<PyCFunction>(py_place), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_mq_torch", nullptr, -1, g_methods};
 

@@ -332,6 +332,54 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+def _place(stream, device):
+    """What a workspace belongs to: the device's index and the stream's address."""
+    if device.type != "cuda":
+        raise ValueError("device tensor expected")
+    return (_calls or _load_calls()).place(stream, -1 if device.index is None else device.index)
+
+
+class _Workspaces:
+    """The workspaces of one object's calls: one per stream, so that calls on
+    several streams may overlap, made and zero-filled on that stream."""
+
+    def __init__(self, keep: bool = False):
+        self.by_place, self.last = {}, None
+        # workspaces that were too small for a later call, if they are to be kept; each is at
+        # least half as large again as the one before, so together they are at most twice the newest
+        self.keep, self.replaced = keep, []
+
+    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
+        place = _place(stream, device)
+        ws = self.by_place.get(place)
+        if ws is None or ws.numel() < nbytes:
+            if ws is not None and self.keep:
+                self.replaced.append(ws)
+                nbytes = max(nbytes, ws.numel() * 3 // 2)
+            with torch.cuda.stream(None if stream is None else _torch_stream(stream, device)):
+                ws = self.by_place[place] = workspace(nbytes, device)
+        self.last = ws
+        return ws
+
+
+class _HasWorkspaces:
+    """`_ws`: the last call's workspace; setting it to None lets all go."""
+
+    _keep_workspaces = False
+
+    def __init__(self):
+        self._spaces = _Workspaces(self._keep_workspaces)
+
+    @property
+    def _ws(self):
+        return self._spaces.last
+
+    @_ws.setter
+    def _ws(self, ws):
+        assert ws is None
+        self._spaces = _Workspaces(self._keep_workspaces)
+
+
 def quantize(x: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> QuantizedTensor:
     """alpha_x of x, then its NVFP4 codes and scales (e.g. offline weight quantization)."""
     rows, K = x.shape
@@ -343,35 +391,36 @@ def quantize(x: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> Qu
     return q
 
 
-class LinearW4A4:
+class LinearW4A4(_HasWorkspaces):
     """A linear layer y = x W^T on the FP4 prefill path: W quantized once at
-    construction, x quantized per call inside mq_linear_w4a4."""
+    construction, x quantized per call inside mq_linear_w4a4.  Calls on
+    different streams may overlap."""
 
     def __init__(self, weight: torch.Tensor):
+        super().__init__()
         assert weight.dtype == torch.bfloat16 and weight.is_cuda
         self.N, self.K = weight.shape
         self.w = quantize(weight.contiguous())
-        self._ws = None
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         M, K = x.shape
         assert K == self.K
-        need = mq_linear_w4a4_workspace_bytes(M, K)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = workspace(need, x.device)
+        ws = self._spaces.get(mq_linear_w4a4_workspace_bytes(M, K), x.device, stream)
         if out is None:
             out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
-        mq_linear_w4a4(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, self._ws, stream)
+        mq_linear_w4a4(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, ws, stream)
         return out
 
 
-class MLPW4A4:
+class MLPW4A4(_HasWorkspaces):
     """A decoder MLP on the FP4 prefill path: y = (SwiGLU(x Wg^T, x Wu^T)) Wd^T
     with both linears W4A4.  The gate and up weights are quantized as one
     [2 inter, K] tensor (gate rows first), the down weight [N, inter] on its
-    own, once at construction; x and H are quantized per call."""
+    own, once at construction; x and H are quantized per call.  Calls on
+    different streams may overlap."""
 
     def __init__(self, w_gate_up: torch.Tensor, w_down: torch.Tensor):
+        super().__init__()
         assert w_gate_up.dtype == torch.bfloat16 and w_down.dtype == torch.bfloat16
         two_inter, self.K = w_gate_up.shape
         self.inter = two_inter // 2
@@ -379,18 +428,14 @@ class MLPW4A4:
         assert two_inter == 2 * self.inter and w_down.shape[1] == self.inter
         self.wgu = quantize(w_gate_up.contiguous())
         self.wd = quantize(w_down.contiguous())
-        self._ws = None
 
-    def workspace(self, M: int, device) -> torch.Tensor:
-        need = mq_mlp_w4a4_workspace_bytes(M, self.K, self.inter)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = workspace(need, device)
-        return self._ws
+    def workspace(self, M: int, device, stream=None) -> torch.Tensor:
+        return self._spaces.get(mq_mlp_w4a4_workspace_bytes(M, self.K, self.inter), torch.device(device), stream)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         M, K = x.shape
         assert K == self.K
-        ws = self.workspace(M, x.device)
+        ws = self.workspace(M, x.device, stream)
         if out is None:
             out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
         mq_mlp_w4a4(x, self.wgu.codes, self.wgu.scales, self.wgu.alpha, self.inter, self.wd.codes, self.wd.scales,
@@ -475,7 +520,7 @@ class PagedKVCache:
         return self.k, self.v, self.k_scale, self.v_scale
 
 
-class AttentionW4A4:
+class AttentionW4A4(_HasWorkspaces):
     """The attention block of a decoder layer, from its input to its O linear:
     QKV linear, rotary positions, append to the paged cache, attention, O
     linear.  The weights are NVFP4; `precise` says whether the linears quantize
@@ -483,23 +528,27 @@ class AttentionW4A4:
     64 rows).
 
     w_qkv [(q heads + 2 kv heads) head_dim, hidden] (q, k, v rows in this
-    order), w_o [hidden, q heads * head_dim]; rope: rope_table(...)."""
+    order), w_o [hidden, q heads * head_dim]; rope: rope_table(...).  Calls on
+    different streams, with caches of their own, may overlap."""
+
+    _keep_workspaces = True
 
     def __init__(self, w_qkv: torch.Tensor, w_o: torch.Tensor, q_heads: int, kv_heads: int, head_dim: int,
                  rope: torch.Tensor, interleaved: bool = False):
+        super().__init__()
         assert w_qkv.shape[0] == (q_heads + 2 * kv_heads) * head_dim and w_o.shape[1] == q_heads * head_dim
         self.qkv, self.o = LinearW4A4(w_qkv), LinearW4A4(w_o)
         self.qkv_precise, self.o_precise = LinearW4A16(self.qkv), LinearW4A16(self.o)
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.rope, self.interleaved = rope, interleaved
-        self._ws, self._kept = None, []
+
+    @property
+    def _kept(self):
+        return self._spaces.replaced
 
     def workspace(self, batch: int, max_q: int, max_len: int, device) -> torch.Tensor:
         need = mq_kv_attention_workspace_bytes(batch, self.q_heads, self.kv_heads, self.head_dim, max_q, max_len)
-        if self._ws is None or self._ws.numel() < need:
-            self._kept.append(self._ws)              # a captured graph may hold its address
-            self._ws = workspace(need, device)
-        return self._ws
+        return self._spaces.get(need, torch.device(device))
 
     def __call__(self, x: torch.Tensor, cache: PagedKVCache, cu_rows, lens, page_table, max_q: int, max_len: int,
                  precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -532,9 +581,15 @@ class AttentionW4A4:
         return (self.o_precise if precise else self.o)(attended.view(T, -1), out)
 
     def status(self, stream=None) -> int:
-        """The workspace's status word (mq_read_status): MQ_ERR_INVALID_ARG when
-        a length, position or page number was outside the tables."""
-        return mq_read_status(self._ws, stream)
+        """The workspaces' status words (mq_read_status), the first that is not
+        MQ_OK: MQ_ERR_INVALID_ARG when a length, position or page number was
+        outside the tables.  Of calls on other streams than `stream` it sees
+        what has ended, or what `stream` waits for."""
+        for ws in self._spaces.by_place.values():
+            status = mq_read_status(ws, stream)
+            if status != MQ_OK:
+                return status
+        return MQ_OK
 
 
 # -- the allocation-free variant (library-owned scratch) ---------------------

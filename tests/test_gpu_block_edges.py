@@ -104,3 +104,57 @@ def test_the_default_stream_by_its_address():
         got = block(x, cache, *args, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def _two(precise, seed):
+    """Two batches for one block: long contexts (split keys), then what each gives alone."""
+    block, T = _block(seed), 3 if precise else 90
+    runs = []
+    for i in range(2):
+        x, cache = _x(T, 20 + i), mq.PagedKVCache(300, P, HKV, D, dev())
+        for t, size in ((cache.k, 448), (cache.v, 448)):
+            t.copy_((torch.randn(t.shape, generator=torch.Generator().manual_seed(i)) * 16).clamp(-size, size).to(t.dtype))
+        table = torch.arange(300, dtype=torch.int32, device=dev())[None]
+        runs.append((x, cache, _i32(0, T), _i32(4000 + 300 * i), table, T, 4700, precise))
+    with torch.cuda.stream(torch.cuda.Stream()):
+        want = [block(*r).clone() for r in runs]                          # appending the same again changes nothing
+    torch.cuda.synchronize()
+    return block, runs, want
+
+
+@pytest.mark.parametrize("precise", [True, False])
+def test_one_block_on_two_streams_at_once(precise):
+    """Each call is as it is alone; the first stream is still busy when the second one's first call begins."""
+    block, runs, want = _two(precise, 7)
+    streams = [torch.cuda.Stream() for _ in runs]
+    outs = [[], []]
+    with torch.cuda.stream(streams[0]):
+        torch.cuda._sleep(10_000_000)                                    # about 5 ms, the workspaces' fill behind it
+    for turn in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(block(*runs[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(y, want[i]) for y in outs[i]), i
+    assert block.status() == mq.MQ_OK
+
+
+def test_workspaces_of_streams():
+    """One per stream, made anew only where a call needs more."""
+    spaces, s = mq._Workspaces(keep=True), torch.cuda.Stream()
+    a = spaces.get(1000, torch.device("cuda"))
+    b = spaces.get(1000, dev(), s)
+    c = spaces.get(1000, dev(), s.cuda_stream)
+    with torch.cuda.stream(s):
+        assert spaces.get(10, dev()) is b is c and spaces.last is b
+    assert a is not b and spaces.get(1000, dev()) is a
+    d = spaces.get(1001, dev())
+    assert d is not a and d.numel() >= 1001 and spaces.replaced == [a]
+    assert spaces.get(1000, dev(), s) is b and spaces.get(1000, dev(), 0) is d
+    torch.cuda.synchronize()
+    assert not b.any() and not d.any()
+    with pytest.raises(ValueError):
+        spaces.get(10, torch.device("cpu"))
+    with pytest.raises(ValueError):
+        spaces.get(10, dev(), "a stream")
