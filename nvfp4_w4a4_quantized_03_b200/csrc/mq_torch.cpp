@@ -7,7 +7,9 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/mq.h"
@@ -234,17 +236,41 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// stream, device index (negative: the current device) -> (device index, the stream's address)
+// stream, device -> what a workspace belongs to: (device index, the stream's
+// address, the id of the graph capture that the stream is in, 0 for none)
 PyObject* py_place(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    long long index;
-    if (!count(n, 2) || !number(args[1], &index)) return nullptr;
+    if (!count(n, 2)) return nullptr;
+    int index = 0;
     void* stream = nullptr;
+    unsigned long long id = 0;
     if (!guarded_void([&] {
-            if (index < 0) index = c10::cuda::current_device();
-            stream = stream_of(args[0], (int)index);
+            if (!THPDevice_Check(args[1])) throw Refused{"device: torch.device expected"};
+            const c10::Device device = reinterpret_cast<THPDevice*>(args[1])->device;
+            if (!device.is_cuda()) throw Refused{"device tensor expected"};
+            index = device.has_index() ? device.index() : c10::cuda::current_device();
+            stream = stream_of(args[0], index);
+            cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+            const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id);
+            if (e != cudaSuccess) {
+                (void)cudaGetLastError();
+                throw std::runtime_error(cudaGetErrorString(e));
+            }
+            if (status != cudaStreamCaptureStatusActive) id = 0;
         }))
         return nullptr;
-    return Py_BuildValue("(LK)", index, (unsigned long long)(uintptr_t)stream);
+    return Py_BuildValue("(iKK)", index, (unsigned long long)(uintptr_t)stream, id);
+}
+
+// Sets what this thread may do while a stream is being captured (a
+// cudaStreamCaptureMode); what it was.
+PyObject* py_capture_mode(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    long long mode;
+    if (!count(n, 1) || !number(args[0], &mode)) return nullptr;
+    return guarded([&] {
+        cudaStreamCaptureMode m = static_cast<cudaStreamCaptureMode>(mode);
+        C10_CUDA_CHECK(cudaThreadExchangeStreamCaptureMode(&m));
+        return static_cast<int>(m);
+    });
 }
 
 PyMethodDef g_methods[] = {
@@ -253,6 +279,7 @@ PyMethodDef g_methods[] = {
     {"append", reinterpret_cast<PyCFunction>(py_append), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(py_attention), METH_FASTCALL, nullptr},
     {"place", reinterpret_cast<PyCFunction>(py_place), METH_FASTCALL, nullptr},
+    {"capture_mode", reinterpret_cast<PyCFunction>(py_capture_mode), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_mq_torch", nullptr, -1, g_methods};
 

@@ -332,33 +332,53 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
-def _place(stream, device):
-    """What a workspace belongs to: the device's index and the stream's address."""
-    if device.type != "cuda":
-        raise ValueError("device tensor expected")
-    return (_calls or _load_calls()).place(stream, -1 if device.index is None else device.index)
-
-
 class _Workspaces:
-    """The workspaces of one object's calls: one per stream, so that calls on
-    several streams may overlap, made and zero-filled on that stream."""
+    """The workspaces of one object's calls: one per stream, made and zero-filled
+    on it, so that calls on several streams may overlap; and one per stream of a
+    graph capture, which no other call uses, so that graphs may overlap with one
+    another and with later calls."""
 
     def __init__(self, keep: bool = False):
         self.by_place, self.last = {}, None
-        # workspaces that were too small for a later call, if they are to be kept; each is at
-        # least half as large again as the one before, so together they are at most twice the newest
+        # workspaces that were too small for a later call: those that a graph holds, and all if
+        # they are to be kept.  Each is at least half as large again as the one before, so those
+        # of a place are together at most twice the newest.
         self.keep, self.replaced = keep, []
 
     def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
-        place = _place(stream, device)
+        place = (_calls or _load_calls()).place(stream, device)
         ws = self.by_place.get(place)
         if ws is None or ws.numel() < nbytes:
-            if ws is not None and self.keep:
+            if ws is not None and (self.keep or place[2]):
                 self.replaced.append(ws)
                 nbytes = max(nbytes, ws.numel() * 3 // 2)
-            with torch.cuda.stream(None if stream is None else _torch_stream(stream, device)):
-                ws = self.by_place[place] = workspace(nbytes, device)
+            if place[2]:
+                ws = self._outside_the_capture(nbytes, place)
+            else:
+                with torch.cuda.stream(None if stream is None else _torch_stream(stream, device)):
+                    ws = workspace(nbytes, device)
+            self.by_place[place] = ws
         self.last = ws
+        return ws
+
+    @staticmethod
+    def _outside_the_capture(nbytes: int, place) -> torch.Tensor:
+        """Zero-filled now, on a stream that is in no capture: a fill in the graph
+        would run at every replay, and not before the first."""
+        device, relaxed = torch.device("cuda", place[0]), 2              # cudaStreamCaptureModeRelaxed
+        mode = _calls.capture_mode(relaxed)
+        try:
+            for _ in range(64):                      # torch hands out the streams of a pool in turn
+                side = torch.cuda.Stream(device)
+                if not _calls.place(side, device)[2]:
+                    break
+            else:
+                raise RuntimeError("no stream outside the capture")
+            with torch.cuda.stream(side):
+                ws = workspace(nbytes, device)
+            side.synchronize()
+        finally:
+            _calls.capture_mode(mode)
         return ws
 
 
@@ -529,7 +549,8 @@ class AttentionW4A4(_HasWorkspaces):
 
     w_qkv [(q heads + 2 kv heads) head_dim, hidden] (q, k, v rows in this
     order), w_o [hidden, q heads * head_dim]; rope: rope_table(...).  Calls on
-    different streams, with caches of their own, may overlap."""
+    different streams and replays of captured ones, with caches of their own,
+    may overlap; a capture's workspaces live as long as the block."""
 
     _keep_workspaces = True
 

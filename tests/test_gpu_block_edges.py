@@ -1,5 +1,6 @@
 """Edges of the attention block (AttentionW4A4): rows that no sequence owns or
-that belong to a refused one, beside the O linear's one tensor scale."""
+that belong to a refused one, beside the O linear's one tensor scale; calls on
+several streams and captured ones, and the workspaces of each."""
 import pytest
 import torch
 
@@ -158,3 +159,81 @@ def test_workspaces_of_streams():
         spaces.get(10, torch.device("cpu"))
     with pytest.raises(ValueError):
         spaces.get(10, dev(), "a stream")
+
+
+@pytest.mark.parametrize("precise", [True, False])
+def test_two_captured_calls_at_once(precise):
+    """Two graphs captured one after the other on the same stream, replayed on two at once, a call on a third."""
+    block, runs, want = _two(precise, 8)
+    ys = [torch.empty_like(w) for w in want]
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(3)]
+    for r, y in zip(runs, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=streams[0]):
+            block(*r, out=y)
+            block(*r, out=y)                                             # the same workspace: one after the other
+    held = {k: ws for k, ws in block._spaces.by_place.items() if k[2]}
+    assert len(held) == 2 and not any(ws.any() for ws in held.values()) and block.status() == mq.MQ_OK
+    third = (runs[0][0], mq.PagedKVCache(300, P, HKV, D, dev()), *runs[0][2:])
+    for t, s in zip(third[1].tensors(), runs[0][1].tensors()):
+        t.copy_(s)
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            y = block(*third)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip([*ys, y], [*want, want[0]]))
+    assert block.status() == mq.MQ_OK
+
+
+@pytest.mark.parametrize("warm", [True, False])
+@pytest.mark.parametrize("precise", [True, False])
+def test_a_captured_call_outlives_larger_ones(precise, warm):
+    """A graph captured at one size, with or without a call before it, then calls that need larger workspaces of every
+    kind, then memory handed out anew: the replay is as before and writes nothing of others."""
+    block, other, table = _block(9), _block(9), torch.arange(300, dtype=torch.int32, device=dev())[None]
+    T = 2 if precise else 20
+    x, cache, y = _x(T, 30), mq.PagedKVCache(300, P, HKV, D, dev()), torch.empty(T, HID, dtype=torch.bfloat16, device=dev())
+    args = (_i32(0, T), _i32(1500), table, T, 1500, precise)
+    want = other(x, mq.PagedKVCache(300, P, HKV, D, dev()), *args)
+    if warm:
+        block(x, cache, *args, out=y)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        block(x, cache, *args, out=y)
+    for stream in (None, s):
+        with torch.cuda.stream(stream):
+            block(_x(900, 31), mq.PagedKVCache(300, P, HKV, D, dev()), _i32(0, 900), _i32(4000), table, 900, 4800)
+    torch.cuda.synchronize()
+    others = [torch.full((n,), 7, dtype=torch.uint8, device=dev()) for n in [1 << k for k in range(9, 22)] * 8]
+    cache.k_scale.fill_(1.0), cache.v_scale.fill_(1.0)
+    cache.k.view(torch.uint8).zero_(), cache.v.view(torch.uint8).zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert all((t == 7).all() for t in others)
+    assert block.status() == mq.MQ_OK
+
+
+def test_a_captured_linear_and_mlp_outlive_larger_calls():
+    lin = mq.LinearW4A4(inputs.weight_bf16(256, HID, seed=1).to(dev()))
+    mlp = mq.MLPW4A4(inputs.weight_bf16(512, HID, seed=2).to(dev()), inputs.weight_bf16(HID, 256, seed=3).to(dev()))
+    x = _x(40, 40)
+    want = [f(x) for f in (lin, mlp)]
+    ys = [torch.empty_like(y) for y in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for f, y in zip((lin, mlp), ys):
+            f(x, y)
+    for f in (lin, mlp):
+        f(_x(3000, 41))
+    others = [torch.full((n,), 7, dtype=torch.uint8, device=dev()) for n in [1 << k for k in range(9, 22)] * 8]
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ys, want)) and all((t == 7).all() for t in others)
