@@ -606,7 +606,7 @@ class AttentionW4A4(_HasWorkspaces):
         MQ_OK: MQ_ERR_INVALID_ARG when a length, position or page number was
         outside the tables.  Of calls on other streams than `stream` it sees
         what has ended, or what `stream` waits for."""
-        for ws in self._spaces.by_place.values():
+        for ws in [*self._spaces.by_place.values(), *self._spaces.replaced]:
             status = mq_read_status(ws, stream)
             if status != MQ_OK:
                 return status

@@ -237,3 +237,15 @@ def test_a_captured_linear_and_mlp_outlive_larger_calls():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ys, want)) and all((t == 7).all() for t in others)
+
+
+def test_status_of_workspaces_that_were_too_small_later():
+    """What a call reported is still there after one that needed a larger workspace; once read, it is gone."""
+    block, table = _block(10), torch.arange(300, dtype=torch.int32, device=dev())[None]
+    assert block.status() == mq.MQ_OK                                    # before the first call
+    cache = mq.PagedKVCache(300, P, HKV, D, dev())
+    block(_x(1), cache, _i32(0, 1), _i32(60), table, 1, 50, True)        # longer than the call allows
+    block(_x(1), cache, _i32(0, 1), _i32(4000), table, 1, 4800, True)
+    assert len(block._kept) == 1
+    assert block.status() == -1
+    assert block.status() == mq.MQ_OK
