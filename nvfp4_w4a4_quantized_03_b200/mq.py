@@ -604,12 +604,14 @@ class AttentionW4A4(_HasWorkspaces):
     def status(self, stream=None) -> int:
         """The workspaces' status words (mq_read_status), the first that is not
         MQ_OK: MQ_ERR_INVALID_ARG when a length, position or page number was
-        outside the tables.  Of calls on other streams than `stream` it sees
+        outside the tables, MQ_ERR_TIMEOUT when a wait in a kernel of the
+        attention or of a quantizing linear ran out.  Of calls on other streams than `stream` it sees
         what has ended, or what `stream` waits for."""
-        for ws in [*self._spaces.by_place.values(), *self._spaces.replaced]:
-            status = mq_read_status(ws, stream)
-            if status != MQ_OK:
-                return status
+        for spaces in (self._spaces, self.qkv._spaces, self.o._spaces):
+            for ws in [*spaces.by_place.values(), *spaces.replaced]:
+                status = mq_read_status(ws, stream)
+                if status != MQ_OK:
+                    return status
         return MQ_OK
 
 

@@ -249,3 +249,13 @@ def test_status_of_workspaces_that_were_too_small_later():
     assert len(block._kept) == 1
     assert block.status() == -1
     assert block.status() == mq.MQ_OK
+
+
+def test_status_of_the_linears_inside():
+    block, table = _block(11), _i32(0, 1)[None]
+    block(_x(20), mq.PagedKVCache(2, P, HKV, D, dev()), _i32(0, 20), _i32(20), table, 20, 32)
+    assert block.status() == mq.MQ_OK
+    for lin in (block.qkv, block.o):
+        lin._ws[8:12].view(torch.int32).fill_(mq.MQ_ERR_TIMEOUT)         # as a product whose wait ran out leaves it
+        assert block.status() == mq.MQ_ERR_TIMEOUT
+        assert block.status() == mq.MQ_OK
