@@ -247,7 +247,9 @@ PyObject* py_place(PyObject*, PyObject* const* args, Py_ssize_t n) {
             if (!THPDevice_Check(args[1])) throw Refused{"device: torch.device expected"};
             const c10::Device device = reinterpret_cast<THPDevice*>(args[1])->device;
             if (!device.is_cuda()) throw Refused{"device tensor expected"};
-            index = device.has_index() ? device.index() : c10::cuda::current_device();
+            index = c10::cuda::current_device();
+            if (device.has_index() && device.index() != index)
+                throw Refused{"tensor on cuda:" + std::to_string(device.index()) + ", but the current device is cuda:" + std::to_string(index)};
             stream = stream_of(args[0], index);
             cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
             const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id);

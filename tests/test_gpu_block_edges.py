@@ -259,3 +259,12 @@ def test_status_of_the_linears_inside():
         lin._ws[8:12].view(torch.int32).fill_(mq.MQ_ERR_TIMEOUT)         # as a product whose wait ran out leaves it
         assert block.status() == mq.MQ_ERR_TIMEOUT
         assert block.status() == mq.MQ_OK
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused():
+    """Before anything is enqueued (the library launches on the current device)."""
+    lin = mq.LinearW4A4(inputs.weight_bf16(64, 64, seed=1).to(dev()))
+    with pytest.raises(ValueError, match="the current device is cuda:0"):
+        lin._spaces.get(256, torch.device("cuda", torch.cuda.device_count()))
+    with pytest.raises(ValueError, match="device tensor expected"):
+        lin(torch.zeros(2, 64, dtype=torch.bfloat16))
