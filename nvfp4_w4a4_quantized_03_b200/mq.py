@@ -214,6 +214,7 @@ def mq_linear_w4a4(x: torch.Tensor, w_codes, w_scales, alpha_w, N: int, y: torch
                    stream=None) -> None:
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and y.dtype == torch.bfloat16
     M, K = x.shape
+    assert y.numel() >= M * N
     _check(lib().mq_linear_w4a4(_ptr(x), M, K, _ptr(w_codes), _ptr(w_scales), _ptr(alpha_w), N, _ptr(y),
                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "mq_linear_w4a4")
 
@@ -235,6 +236,7 @@ def mq_mlp_w4a4(x: torch.Tensor, wgu_codes, wgu_scales, alpha_gu, inter: int, wd
                 N: int, y: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and y.dtype == torch.bfloat16
     M, K = x.shape
+    assert y.numel() >= M * N
     _check(lib().mq_mlp_w4a4(_ptr(x), M, K, _ptr(wgu_codes), _ptr(wgu_scales), _ptr(alpha_gu), inter,
                              _ptr(wd_codes), _ptr(wd_scales), _ptr(alpha_d), N, _ptr(y), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream(stream)), "mq_mlp_w4a4")
