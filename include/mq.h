@@ -297,7 +297,7 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  *             (host values, e.g. fixed for a captured graph; one that has
  *             more sets MQ_ERR_INVALID_ARG in the workspace's status word and
  *             its rows are not written)
- *   scale   : finite and positive
+ *   scale   : positive, at most 2^127
  *   ws      : >= mq_kv_attention_workspace_bytes(batch, q_heads, kv_heads,
  *             head_dim, max_q, max_len) bytes, 256-byte aligned, zero-filled
  *             before its first use and used by mq_kv_attention alone (calls

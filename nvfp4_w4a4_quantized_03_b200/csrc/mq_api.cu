@@ -460,7 +460,7 @@ int mq_kv_attention(const void* q, int64_t T, int64_t q_row_stride, int32_t q_he
         return MQ_ERR_SHAPE;
     if (q_row_stride < (int64_t)q_heads * cache->head_dim || q_row_stride % 8 != 0 || q_row_stride > (int64_t)1 << 32)
         return MQ_ERR_SHAPE;
-    if (!(scale > 0.f) || scale > 3.0e38f) return MQ_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > 0x1p127f) return MQ_ERR_INVALID_ARG;         // times log2(e) it is still finite
     const mq::KvPlan plan =
         mq::kv_plan(batch->batch, q_heads, cache->kv_heads, cache->head_dim, max_q, max_len);
     if (!ws || ws_bytes < (size_t)plan.bytes) return MQ_ERR_WORKSPACE;
