@@ -119,6 +119,13 @@ int32_t int32_of(int64_t v, const char* what) {
     return (int32_t)v;
 }
 
+// Lets other Python threads run while it lives: a launch waits where its
+// stream's queue is full.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs f, with its refusals and torch's exceptions as Python errors; false with one.
 template <typename F>
 bool guarded_void(F f) {
@@ -175,7 +182,9 @@ PyObject* py_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (N < 0 || c.numel() < N * (K / 2) || s.numel() < (N + 127) / 128 * 128 * ((K + 63) / 64 * 4) || alpha.numel() < 1)
             throw Refused{"w_codes, w_scales, alpha_w: smaller than an [N, K] weight's"};
         if (y.numel() < M * N) throw Refused{"y: smaller than [M, N]"};
-        return g_linear(ptr(x), M, K, ptr<uint8_t>(c), ptr<uint8_t>(s), ptr<float>(alpha), N, ptr(y), stream_of(args[6], dev));
+        void* stream = stream_of(args[6], dev);
+        Unlocked unlocked;
+        return g_linear(ptr(x), M, K, ptr<uint8_t>(c), ptr<uint8_t>(s), ptr<float>(alpha), N, ptr(y), stream);
     });
 }
 
@@ -210,9 +219,12 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
             ws = ptr(w);
             ws_bytes = (size_t)w.numel();
         }
-        return g_append(ptr(qkv), q.size(0), row_stride(qkv, "qkv", qkv.size(1)), int32_of(q.size(1), "q_out"), rope, positions,
-                        int32_of(rot_dim >= 0 ? rot_dim : columns, "rot_dim"), interleaved, &kv.cache, &kv.batch, ptr(q), ws,
-                        ws_bytes, stream_of(args[13], dev));
+        const int64_t T = q.size(0), stride = row_stride(qkv, "qkv", qkv.size(1));
+        const int32_t heads = int32_of(q.size(1), "q_out"), rot = int32_of(rot_dim >= 0 ? rot_dim : columns, "rot_dim");
+        void* stream = stream_of(args[13], dev);
+        Unlocked unlocked;
+        return g_append(ptr(qkv), T, stride, heads, rope, positions, rot, interleaved, &kv.cache, &kv.batch, ptr(q), ws,
+                        ws_bytes, stream);
     });
 }
 
@@ -230,9 +242,12 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor& ws = need(args[9], "ws", at::kByte, dev);
         if (q.dim() != 3 || q.size(2) != kv.cache.head_dim || out.sizes() != q.sizes())
             throw Refused{"q and out [T, q heads, head_dim] do not agree with the cache"};
-        return g_attention(ptr(q), q.size(0), row_stride(q, "q", q.size(1) * q.size(2)), int32_of(q.size(1), "q"), &kv.cache,
-                           &kv.batch, max_q, max_len, (float)scale, ptr(out), ptr(ws), (size_t)ws.numel(),
-                           stream_of(args[13], dev));
+        const int64_t T = q.size(0), stride = row_stride(q, "q", q.size(1) * q.size(2));
+        const int32_t heads = int32_of(q.size(1), "q");
+        void* stream = stream_of(args[13], dev);
+        Unlocked unlocked;
+        return g_attention(ptr(q), T, stride, heads, &kv.cache, &kv.batch, max_q, max_len, (float)scale, ptr(out), ptr(ws),
+                           (size_t)ws.numel(), stream);
     });
 }
 
