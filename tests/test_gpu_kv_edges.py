@@ -1,6 +1,7 @@
 """Edges of the attention over the paged E4M3 cache (mq_kv_attention), in the
 form for few rows and in the tcgen05 form: a NaN at every place of a group of 16
-keys, page numbers outside the pool.  Plain forms and bounds as in test_gpu_kv."""
+keys, page numbers outside the pool, partial results joined at either head
+dimension, page scales far apart.  Plain forms and bounds as in test_gpu_kv."""
 import pytest
 import torch
 
@@ -75,3 +76,29 @@ def test_keys_of_a_page_outside_the_pool_are_left_out(new, length, head_dim, num
     got = _attend(bt, d, q, 0.125, status=-1)
     assert (got[new:2 * new] == 0).all()
     kv.close_to(got, want, bound)
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("seqs,group", [([(20, 3000)], 1), ([(33, 2500)], 2), ([(60, 4000), (3, 1100), (25, 30)], 1),
+                                        ([(65, 2049)], 4), ([(300, 5000)], 2), ([(1, 9000)], 4), ([(2, 20000), (1, 17)], 8)])
+def test_joined_chunks(seqs, group, head_dim):
+    """Keys split over blocks and joined, up to 64 rows per cell (a warp per row) and more (a thread per row)."""
+    bt = kv.Batch(seqs, 16, 2, head_dim, seed=len(seqs) + group).fill()
+    q = _q(bt, 2 * group, group)
+    got = _attend(bt, bt.to(dev()), q, bt.D ** -0.5)
+    kv.close_to(got, *kv.attention_plain(bt, q, bt.D ** -0.5))
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_of_zeros_beside_large_ones(new, head_dim):
+    """V all zero (the least scale there is, 2^-96) beside V up to 448 2^12: the zeros keep their share of the softmax."""
+    bt = kv.Batch([(new, 96)], 16, 1, head_dim, seed=3).fill()
+    for i in (1, 3):
+        p = int(bt.table[0, i])
+        bt.v[p], bt.vs[p] = 0, 2.0 ** -96
+    p = int(bt.table[0, 0])
+    bt.vs[p] *= 2.0 ** 12 / float(bt.vs[p])
+    q = _q(bt, 2, 4)
+    got = _attend(bt, bt.to(dev()), q, 0.125)
+    kv.close_to(got, *kv.attention_plain(bt, q, 0.125))
