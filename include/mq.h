@@ -288,7 +288,10 @@ int mq_linear_w4a16(const void *x, int64_t M, int64_t K,
  * such j, and the workspace's status word takes MQ_ERR_INVALID_ARG.
  * Products are of f16 operands (the cache's codes are exact in f16, q goes to
  * f16 under a power of two per row, the softmax weights round to f16), sums
- * and statistics in binary32, the output rounded once to bf16.
+ * and statistics in binary32, the output rounded once to bf16.  A key counts
+ * as nothing where its softmax weight times its page's V scale is below 2^-118
+ * of the row's largest such product (V scales of a sequence's head 2^100 and
+ * more apart).
  *   q       : device bf16 [T, q_row_stride], a row's heads at its front;
  *             q_row_stride >= q_heads head_dim, a multiple of 8
  *   out     : device bf16 [T, q_heads, head_dim], written; it may not overlap q

@@ -17,9 +17,8 @@
 // Bound: memory (one read of the product, one write of Q and of the codes).  One
 // block per (page, kv head) finds the page's maximum and then writes its codes;
 // the Q rows ride in the same launch.  8192 tokens of 32 + 2 x 8 heads of 128
-// (189 MB algorithmic): 44 us, 4.2 TB/s, of which the Q rows alone take 31 us
-// and K and V alone 18 us; one token of one sequence 2.9 us, of 64 sequences
-// 4.3 us.
+// (189 MB algorithmic): 42 us, 4.5 TB/s (the Q rows alone take 31 us, K and V
+// alone 18); one token of one sequence 3.1 us, of 64 sequences 4.1 us (in a graph).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -12,16 +12,20 @@
 // to f16 after division by its row's power of two, which loses nothing above
 // 2^-38 of the row's maximum; so the f16 products are those of the exact
 // operands, and the one rounding is that of the weights to f16 (2^-12).
-// Scores, weights, sums and outputs are held in binary32.
+// Scores, weights, sums and outputs are held in binary32.  A weight below 2^-126
+// is zero: a key is lost, from the denominator too, where 2^(u_j) is less than
+// 2^-118 of the row's largest (6 + 8 bits of room above the maximum); with V's
+// page scales within 2^100 of one another that is a key of no weight.
 //
 // Bound: the cache is read once per kv head (2 D bytes per token), at HBM
 // rate: 64 sequences of up to 8K tokens, 32 / 8 heads of 128, 106 us (4.8 TB/s,
-// 0.73 of the measured copy), 4 of 131K 198 us (5.4 TB/s); at D = 64 the
-// instructions per byte double, 3.0 TB/s.  One sequence of 4K takes 11 us, most
-// of it the chain of dependent loads (lengths, page, codes) and the join.  A warp takes 16 tokens at a time straight from global memory into
-// the fragments of mma.m16n8k16: K's codes as the left operand (tokens x d),
-// V's as the left operand of the second product (d x tokens); the order of d
-// inside a fragment is free, so each lane loads 16 consecutive bytes of a
+// 0.73 of the measured copy), 4 of 131K 197 to 207 us (box to box, 5.2 to 5.4
+// TB/s); at D = 64 the instructions per byte double, 3.0 TB/s.  One sequence of
+// 4K takes 12 us, most of it the chain of dependent loads (lengths, page, codes)
+// and the join.  A warp takes 16 tokens at a time straight from global memory
+// into the fragments of mma.m16n8k16: K's codes as the left operand (tokens x
+// d), V's as the left operand of the second product (d x tokens); the order of
+// d inside a fragment is free, so each lane loads 16 consecutive bytes of a
 // token.  The transposition of the weights between the two products is one
 // movmatrix per 8 x 8.  Nothing goes through shared memory but the merge of
 // the warps' partial results.

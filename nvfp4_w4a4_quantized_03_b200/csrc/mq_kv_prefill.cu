@@ -15,7 +15,10 @@
 //                    the left operand of the second product
 //   warps 8-11       converters: E4M3 codes from global memory to f16 in shared
 //                    memory (128-byte swizzle), one block ahead in registers
-//   warp 13          looks up the pages and scales of the blocks to come
+//   warp 13          looks up the pages and scales of the blocks to come; a group
+//                    of 16 keys without a page is read from zeros and gets no
+//                    weight (addresses from here on: zeroing in the converters
+//                    cost 3% of a prompt's time, they are short of registers)
 //   warp 12          issues the products: S_t = Q_t K^T, then O_t += P_t V, the
 //                    two tiles alternating, so that one tile's softmax runs
 //                    under the other's products
@@ -25,7 +28,7 @@
 // tensor pipe at D = 128 and their 32768 exponentials 2048 cycles of the SFU;
 // a tile's own chain (products 1420 cycles, scores and maximum 550, weights
 // 1750, hand-overs) is ~4000, and two tiles in turn leave either pipe about
-// half idle: 8192-token prompt, 32 heads of 128: 0.61 ms, 900 TFLOP/s.
+// half idle: 8192-token prompt, 32 heads of 128: 0.60 ms, 920 TFLOP/s.
 // Measured against this form and dropped (same prompt): two threads per row
 // (0.69 ms), the weights under the last block's maximum, computed again where it
 // rose (0.65 ms), an issuer of its own for each tile (0.73 ms; 0.63 ms with the

@@ -2,8 +2,9 @@
 // microseconds (mq_linear_w4a16, mq_rope_kv_append, mq_kv_attention): the
 // checks and the marshalling of mq.py's other calls, natively, because in
 // Python they take longer than the kernels (10.6 us of host time for an append
-// through ctypes).  It calls the library that mq.py has loaded (release or
-// debug build) through the addresses given to bind(), and holds nothing else.
+// through ctypes); and what mq.py asks about streams for its workspaces.  It calls
+// the library that mq.py has loaded (release or debug build) through the
+// addresses given to bind(), and holds nothing else.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

@@ -14,9 +14,9 @@
 // Bound: the weight is read once (0.5625 bytes per element), but its decoding
 // keeps up with memory only just: ~180 instructions per 16 rows x 128 columns
 // of a warp, 2 cycles each on the ALU.  Measured: 1 x 4096 x 4096 5.1 us, 1 x
-// 6144 x 4096 6.8, 1 x 24576 x 4096 17.9 (3.2 TB/s; 14.6 with the arithmetic
+// 6144 x 4096 6.8, 1 x 24576 x 4096 18.0 (3.2 TB/s; 14.6 with the arithmetic
 // left out, 12.3 with the loads left out), 5 x 24576 x 4096 19.3, 32 x 4096 x
-// 12288 22.5.  A block holds 128 rows of W and one slice of K, the blocks of a
+// 12288 22.2.  A block holds 128 rows of W and one slice of K, the blocks of a
 // cluster the slices of the same rows; a block's partial sums are added through
 // distributed shared memory in rank order.  Each lane reads 16 bytes (32
 // elements, two scale blocks) of a row at a time, four steps ahead, and the
