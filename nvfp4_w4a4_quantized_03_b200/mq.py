@@ -402,6 +402,20 @@ class _HasWorkspaces:
         self._spaces = _Workspaces(self._keep_workspaces)
 
 
+def _output(out, shape, device, stream) -> torch.Tensor:
+    """`out`, or a new tensor: of the call's stream, since memory that the current
+    one gave back may still be in use there, and not handed out again before
+    what the current one holds when it is let go."""
+    if out is not None:
+        return out
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def quantize(x: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> QuantizedTensor:
     """alpha_x of x, then its NVFP4 codes and scales (e.g. offline weight quantization)."""
     rows, K = x.shape
@@ -428,8 +442,7 @@ class LinearW4A4(_HasWorkspaces):
         M, K = x.shape
         assert K == self.K
         ws = self._spaces.get(mq_linear_w4a4_workspace_bytes(M, K), x.device, stream)
-        if out is None:
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+        out = _output(out, (M, self.N), x.device, stream)
         mq_linear_w4a4(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, ws, stream)
         return out
 
@@ -458,8 +471,7 @@ class MLPW4A4(_HasWorkspaces):
         M, K = x.shape
         assert K == self.K
         ws = self.workspace(M, x.device, stream)
-        if out is None:
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+        out = _output(out, (M, self.N), x.device, stream)
         mq_mlp_w4a4(x, self.wgu.codes, self.wgu.scales, self.wgu.alpha, self.inter, self.wd.codes, self.wd.scales,
                     self.wd.alpha, self.N, out, ws, stream)
         return out
@@ -485,8 +497,7 @@ class LinearW4A16:
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         M, K = x.shape
         assert K == self.K
-        if out is None:
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+        out = _output(out, (M, self.N), x.device, stream)
         mq_linear_w4a16(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, stream)
         return out
 
