@@ -418,12 +418,18 @@ def _output(out, shape, device, stream) -> torch.Tensor:
 
 def quantize(x: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> QuantizedTensor:
     """alpha_x of x, then its NVFP4 codes and scales (e.g. offline weight quantization)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream, x.device)):
+            q = quantize(x, ws)
+        for t in (q.codes, q.scales, q.alpha):
+            t.record_stream(torch.cuda.current_stream(x.device))
+        return q
     rows, K = x.shape
     q = QuantizedTensor(rows, K, x.device)
     if ws is None:
         ws = workspace(mq_workspace_bytes(), x.device)
-    mq_tensor_scale(x, q.alpha, ws, stream)
-    mq_nvfp4_quantize(x, q.alpha, q.codes, q.scales, stream)
+    mq_tensor_scale(x, q.alpha, ws)
+    mq_nvfp4_quantize(x, q.alpha, q.codes, q.scales)
     return q
 
 

@@ -43,3 +43,20 @@ def test_an_output_on_another_stream(make):
         others = [torch.full((M, N), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(read, want) and all((o == 7.0).all() for o in others)
+
+
+def test_quantize_on_another_stream():
+    """Its tensors and its workspace are that stream's: the current one is busy meanwhile."""
+    x, s = _w(256, K, 3), torch.cuda.Stream()
+    want = mq.quantize(x)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device=dev()) for n in [1 << k for k in range(4, 20)] * 2]
+    torch.cuda.synchronize()
+    del junk
+    torch.cuda._sleep(50_000_000)                                        # about 25 ms
+    got = mq.quantize(x, stream=s)
+    s.synchronize()
+    parts = [(got.codes, want.codes), (got.scales, want.scales), (got.alpha, want.alpha)]
+    with torch.cuda.stream(s):
+        assert all(torch.equal(a, b) for a, b in parts)
