@@ -342,12 +342,22 @@ class _Workspaces:
 
     def __init__(self, keep: bool = False):
         self.by_place, self.last = {}, None
+        self.sizes, self.nbytes = None, 0
         # workspaces that were too small for a later call: those that a graph holds, and all if
         # they are to be kept.  Each is at least half as large again as the one before, so those
         # of a place are together at most twice the newest.
         self.keep, self.replaced = keep, []
 
+    def of(self, bytes_of, sizes, device, stream=None) -> torch.Tensor:
+        """get() of the bytes of a call of these sizes (asking the library takes a
+        microsecond, and calls of the same sizes follow one another)."""
+        if sizes != self.sizes:
+            self.sizes, self.nbytes = sizes, bytes_of(*sizes)
+        return self.get(self.nbytes, device, stream)
+
     def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
+        if not isinstance(device, torch.device):
+            device = torch.device(device)
         place = (_calls or _load_calls()).place(stream, device)
         ws = self.by_place.get(place)
         if ws is None or ws.numel() < nbytes:
@@ -447,7 +457,7 @@ class LinearW4A4(_HasWorkspaces):
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         M, K = x.shape
         assert K == self.K
-        ws = self._spaces.get(mq_linear_w4a4_workspace_bytes(M, K), x.device, stream)
+        ws = self._spaces.of(mq_linear_w4a4_workspace_bytes, (M, K), x.device, stream)
         out = _output(out, (M, self.N), x.device, stream)
         mq_linear_w4a4(x, self.w.codes, self.w.scales, self.w.alpha, self.N, out, ws, stream)
         return out
@@ -471,7 +481,7 @@ class MLPW4A4(_HasWorkspaces):
         self.wd = quantize(w_down.contiguous())
 
     def workspace(self, M: int, device, stream=None) -> torch.Tensor:
-        return self._spaces.get(mq_mlp_w4a4_workspace_bytes(M, self.K, self.inter), torch.device(device), stream)
+        return self._spaces.of(mq_mlp_w4a4_workspace_bytes, (M, self.K, self.inter), device, stream)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         M, K = x.shape
@@ -587,8 +597,8 @@ class AttentionW4A4(_HasWorkspaces):
         return self._spaces.replaced
 
     def workspace(self, batch: int, max_q: int, max_len: int, device) -> torch.Tensor:
-        need = mq_kv_attention_workspace_bytes(batch, self.q_heads, self.kv_heads, self.head_dim, max_q, max_len)
-        return self._spaces.get(need, torch.device(device))
+        return self._spaces.of(mq_kv_attention_workspace_bytes,
+                               (batch, self.q_heads, self.kv_heads, self.head_dim, max_q, max_len), device)
 
     def __call__(self, x: torch.Tensor, cache: PagedKVCache, cu_rows, lens, page_table, max_q: int, max_len: int,
                  precise: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -607,7 +617,7 @@ class AttentionW4A4(_HasWorkspaces):
         T = x.shape[0]
         if self.rope is not None:
             # the append leaves the rows of positions behind the table's: so does the attention
-            max_len = min(max_len, self.rope.shape[0])
+            max_len = min(max_len, self.rope.size(0))
         ws = self.workspace(page_table.shape[0], max_q, max_len, x.device)
         q = torch.empty(T, self.q_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
         # the quantizing O linear takes one tensor scale over all rows, those too
