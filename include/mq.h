@@ -393,7 +393,8 @@ int mq_debug_bounds_hits(int64_t *hits);
 
 /*
  * Synchronizes `stream`, then reads the status word of a workspace into
- * *device_status (MQ_OK or MQ_ERR_TIMEOUT) and clears it.  `ws` is a device
+ * *device_status (MQ_OK, MQ_ERR_TIMEOUT, or the MQ_ERR_INVALID_ARG of
+ * mq_rope_kv_append and mq_kv_attention) and clears it.  `ws` is a device
  * pointer, `device_status` a host pointer.
  */
 int mq_read_status(void *ws, void *stream, int32_t *device_status);

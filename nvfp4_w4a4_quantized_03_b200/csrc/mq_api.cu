@@ -533,7 +533,8 @@ int mq_read_status(void* ws, void* stream, int32_t* device_status) {
     int32_t v = 0;
     if (cudaStreamSynchronize(s) != cudaSuccess) return MQ_ERR_CUDA;
     if (cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return MQ_ERR_CUDA;
-    if (cudaMemset(word, 0, sizeof v) != cudaSuccess) return MQ_ERR_CUDA;
+    // a word that reads MQ_OK stays: a kernel on another stream may be about to set it
+    if (v != MQ_OK && cudaMemset(word, 0, sizeof v) != cudaSuccess) return MQ_ERR_CUDA;
     *device_status = v;
     return MQ_OK;
 }
